@@ -242,6 +242,103 @@ int qlora_linear_bwd(const nf4_tensor* w, const uint16_t* A, const uint16_t* B, 
                      uint16_t* dB, int accumulate_grads, void* ws, size_t ws_bytes,
                      void* stream);
 
+/* ---------------------------------------------------------------- adapter dropout */
+
+/*
+ * Dropout on the adapter's input, the mask never stored: keep decisions come
+ * from a counter-based generator and are generated again by the backward.
+ *   p      drop probability, 0 <= p < 1, rounded to a multiple of 2^-15:
+ *          t = floor(p 2^15 + 1/2), kept values are scaled by
+ *          2^15 / (2^15 - t).  p that rounds to 0 drops nothing (state may be
+ *          NULL); p that rounds to 1 is refused.
+ *   state  {seed, offset}: two int64 in DEVICE memory, 8-byte aligned, read
+ *          when the kernels run, so that a captured graph draws a new mask
+ *          whenever the caller (or a node of the graph) has changed them.  The
+ *          forward and the backward of one layer call must see the same state;
+ *          different layers and steps need different ones.
+ * Generator: Philox4x32, 7 rounds (Salmon, Moraes, Dror and Shaw, SC 2011),
+ * key = seed (low, high word), counter = (group low, group high, offset low,
+ * offset high), group = flat element index / 8.  The eight elements of a group
+ * take the low and high halves of the four output words in order; an element
+ * is kept iff the low 15 bits of its half are >= t.
+ */
+typedef struct {
+    double p;
+    const int64_t* state;
+} lora_dropout_params;
+
+#define NF4_DTYPE_BF16 0
+#define NF4_DTYPE_F32 1
+
+/*
+ * lora_dropout -- out_i = keep_i X_i scale over n elements of `dtype`
+ * (bfloat16 as uint16_t, or float): computed in fp32, rounded once; a dropped
+ * element is 0 whatever X held.  The gradient is the same call on the incoming
+ * gradient.  Element i of an [M, d_in] array here is element i of X in the
+ * layer calls below: the same state gives the same mask.  out may be X.
+ * n = 0 does nothing.
+ */
+int lora_dropout(const void* X, int64_t n, int dtype, const lora_dropout_params* dropout, void* out, void* stream);
+
+/*
+ * qlora_linear_dropout_fwd / _bwd -- the layer with dropout on the adapter's
+ * input, D = keep .* X * scale (the base product sees X itself):
+ *   T  = s D A^T              Y  = X W_hat^T + T B^T
+ *   V  = s dY B               dX = dY W_hat + keep .* (V A) * scale
+ *   dA = V^T D                dB = dY^T T
+ * D is never formed in memory.  dropout NULL or p = 0 is the plain layer (its
+ * own kernels: results agree with qlora_linear_fwd / _bwd to rounding, not bit
+ * for bit).  A value that is dropped cannot reach T or dA, nor V A reach a
+ * dropped element of dX, even if it is a NaN or infinite.  Everything else as
+ * for qlora_linear_fwd / _bwd: shapes, T_saved, NULL outputs,
+ * accumulate_grads, M = 0; ws >= the sizes below.
+ */
+size_t qlora_linear_dropout_fwd_workspace_bytes(int64_t M, int64_t d_out, int64_t d_in, int r);
+size_t qlora_linear_dropout_bwd_workspace_bytes(int64_t M, int64_t d_out, int64_t d_in, int r);
+int qlora_linear_dropout_fwd(const nf4_tensor* w, const uint16_t* A, const uint16_t* B, int r, float scaling,
+                             const lora_dropout_params* dropout, const uint16_t* X, int64_t M, uint16_t* Y,
+                             float* T_saved, void* ws, size_t ws_bytes, void* stream);
+int qlora_linear_dropout_bwd(const nf4_tensor* w, const uint16_t* A, const uint16_t* B, int r, float scaling,
+                             const lora_dropout_params* dropout, const uint16_t* X, const float* T_saved,
+                             const uint16_t* dY, int64_t M, uint16_t* dX, uint16_t* dA, uint16_t* dB,
+                             int accumulate_grads, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- experts */
+
+#define NF4_MAX_EXPERTS 4096
+
+/*
+ * qlora_grouped_fwd / _bwd -- the layer of a mixture of experts: n_experts
+ * weights and adapters of one shape, the rows of the batch sorted by expert.
+ *   w        the experts' weights stacked and encoded as one tensor
+ *            [n_experts * d_out, d_in] (nf4_quantize takes it as it is; with
+ *            double quantisation the group scales and the mean are shared)
+ *   A, B     [n_experts, r, d_in] and [n_experts, d_out, r]; dA, dB alike
+ *   offsets  [n_experts + 1] int32, DEVICE, 0 <= offsets[0] <= ... <=
+ *            offsets[n_experts] <= M: expert e has the rows offsets[e] ..
+ *            offsets[e + 1] - 1 of X, Y, T_saved, dY and dX
+ * with the formulas of the dropout layer (dropout may be NULL) per group.  An
+ * expert may have no rows: its weight is not read, its dA and dB are zero (or
+ * left as they are when accumulating).  Rows before offsets[0] and from
+ * offsets[n_experts] on are not read into any result, and Y, T_saved and dX
+ * keep what they held there.  The dropout element index counts all of X
+ * [M, d_in].  Nothing is copied to the host: the grid covers the most row
+ * tiles that M rows in n_experts groups can need.
+ * Offsets that break the rule lead no access out of the arrays; the results
+ * are then undefined, and nf4lora_device_status() returns NF4_ERR_INVALID_ARG.
+ * Requirements: 1 <= n_experts <= NF4_MAX_EXPERTS, d_out % 8 == 0; else as for
+ * qlora_linear_fwd / _bwd, ws >= the sizes below (d_out of one expert).
+ */
+size_t qlora_grouped_fwd_workspace_bytes(int64_t M, int n_experts, int64_t d_out, int64_t d_in, int r);
+size_t qlora_grouped_bwd_workspace_bytes(int64_t M, int n_experts, int64_t d_out, int64_t d_in, int r);
+int qlora_grouped_fwd(const nf4_tensor* w, int n_experts, const uint16_t* A, const uint16_t* B, int r, float scaling,
+                      const lora_dropout_params* dropout, const uint16_t* X, int64_t M, const int32_t* offsets,
+                      uint16_t* Y, float* T_saved, void* ws, size_t ws_bytes, void* stream);
+int qlora_grouped_bwd(const nf4_tensor* w, int n_experts, const uint16_t* A, const uint16_t* B, int r, float scaling,
+                      const lora_dropout_params* dropout, const uint16_t* X, const float* T_saved,
+                      const uint16_t* dY, int64_t M, const int32_t* offsets, uint16_t* dX, uint16_t* dA, uint16_t* dB,
+                      int accumulate_grads, void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- adapter merge */
 
 /* Workspace (device bytes, 256-byte aligned) of nf4_merge_requantize: the
@@ -329,8 +426,9 @@ int lora_adamw_step(const lora_adamw_tensor* tensors, int count, const lora_adam
 const char* nf4lora_last_error_string(void);
 
 /* Reads (and clears) the device status word of the current device after
- * synchronising `stream`: NF4_OK, or NF4_ERR_TIMEOUT if a kernel gave up a
- * bounded wait since the last call.  Returns NF4_ERR_CUDA if the
+ * synchronising `stream`: NF4_OK, NF4_ERR_TIMEOUT if a kernel gave up a
+ * bounded wait since the last call, or NF4_ERR_INVALID_ARG if a grouped call
+ * met offsets that break its rule.  Returns NF4_ERR_CUDA if the
  * synchronisation fails. */
 int nf4lora_device_status(void* stream);
 

@@ -34,6 +34,10 @@ ABI_SYMBOLS = ("nf4_packed_bytes", "nf4_tensor_from_buffer", "nf4_packed_bytes_n
                "nf4_tensor_from_buffer_nodq", "nf4_quantize_workspace_bytes",
                "qlora_fwd_workspace_bytes", "qlora_bwd_workspace_bytes", "nf4_quantize",
                "nf4_quantize_noalloc", "nf4_dequantize", "qlora_linear_fwd", "qlora_linear_bwd",
+               "lora_dropout", "qlora_linear_dropout_fwd_workspace_bytes",
+               "qlora_linear_dropout_bwd_workspace_bytes", "qlora_linear_dropout_fwd",
+               "qlora_linear_dropout_bwd", "qlora_grouped_fwd_workspace_bytes",
+               "qlora_grouped_bwd_workspace_bytes", "qlora_grouped_fwd", "qlora_grouped_bwd",
                "nf4_merge_workspace_bytes", "nf4_merge_lora", "nf4_merge_requantize",
                "lora_adamw_step", "nf4lora_last_error_string", "nf4lora_device_status", "nf4lora_check_bounded_wait",
                "nf4lora_debug_site", "nf4lora_debug_build", "nf4lora_trace_start",
@@ -45,6 +49,10 @@ class Nf4TensorStruct(ctypes.Structure):
                 ("codes", ctypes.c_void_p), ("qscale", ctypes.c_void_p),
                 ("scale2", ctypes.c_void_p), ("scale_mean", ctypes.c_void_p),
                 ("absmax", ctypes.c_void_p)]
+
+
+class LoraDropoutStruct(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("state", ctypes.c_void_p)]
 
 
 class AdamwTensorStruct(ctypes.Structure):
@@ -71,6 +79,7 @@ def _load() -> ctypes.CDLL:
     P, I64, SZ, I, F = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int,
                         ctypes.c_float)
     S = ctypes.POINTER(Nf4TensorStruct)
+    D = ctypes.POINTER(LoraDropoutStruct)
     sig = {
         "nf4_packed_bytes": (SZ, [I64, I64]),
         "nf4_tensor_from_buffer": (I, [S, P, SZ, I64, I64]),
@@ -84,6 +93,15 @@ def _load() -> ctypes.CDLL:
         "nf4_dequantize": (I, [S, P, P]),
         "qlora_linear_fwd": (I, [S, P, P, I, F, P, I64, P, P, P, SZ, P]),
         "qlora_linear_bwd": (I, [S, P, P, I, F, P, P, P, I64, P, P, P, I, P, SZ, P]),
+        "lora_dropout": (I, [P, I64, I, D, P, P]),
+        "qlora_linear_dropout_fwd_workspace_bytes": (SZ, [I64, I64, I64, I]),
+        "qlora_linear_dropout_bwd_workspace_bytes": (SZ, [I64, I64, I64, I]),
+        "qlora_linear_dropout_fwd": (I, [S, P, P, I, F, D, P, I64, P, P, P, SZ, P]),
+        "qlora_linear_dropout_bwd": (I, [S, P, P, I, F, D, P, P, P, I64, P, P, P, I, P, SZ, P]),
+        "qlora_grouped_fwd_workspace_bytes": (SZ, [I64, I, I64, I64, I]),
+        "qlora_grouped_bwd_workspace_bytes": (SZ, [I64, I, I64, I64, I]),
+        "qlora_grouped_fwd": (I, [S, I, P, P, I, F, D, P, I64, P, P, P, P, SZ, P]),
+        "qlora_grouped_bwd": (I, [S, I, P, P, I, F, D, P, P, P, I64, P, P, P, P, I, P, SZ, P]),
         "nf4_merge_workspace_bytes": (SZ, [I64, I64]),
         "nf4_merge_lora": (I, [S, P, P, I, F, P, P]),
         "nf4_merge_requantize": (I, [S, P, P, I, F, S, P, SZ, P]),
@@ -301,6 +319,188 @@ def qlora_linear_bwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, scaling: fl
                                 1 if accumulate else 0, _ptr(ws), 0 if ws is None else ws.numel(),
                                 _stream()))
     return dX, dA, dB
+
+
+# ---------------------------------------------------------------- adapter dropout, experts
+def _matrix(t: Optional[torch.Tensor], name: str, dtype, shape, device) -> Optional[torch.Tensor]:
+    """`t` checked to be a contiguous CUDA tensor of this type, shape and device."""
+    if t is not None and (t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape)
+                          or t.device != device):
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
+                         % (name, str(dtype).replace("torch.", ""), list(shape), device))
+    return t
+
+
+def _dropout(p: float, rng: Optional[torch.Tensor], device) -> LoraDropoutStruct:
+    """The generator's state is a CUDA int64 tensor (seed, offset), read when
+    the kernels run."""
+    if rng is not None:
+        _matrix(rng, "rng", torch.int64, (2,), device)
+    return LoraDropoutStruct(float(p), None if rng is None else rng.data_ptr())
+
+
+def lora_dropout(X: torch.Tensor, p: float, rng: Optional[torch.Tensor],
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """keep .* X / (1 - p) for a contiguous bfloat16 or float32 CUDA tensor;
+    no mask is stored: the keep decisions are a function of rng = (seed,
+    offset), a CUDA int64 tensor, and the element's index (lora_dropout_params
+    in include/nf4lora.h).  The gradient is the same call on the incoming
+    gradient.  `out` may be X."""
+    if X.dtype not in (torch.bfloat16, torch.float32) or not X.is_cuda or not X.is_contiguous():
+        raise ValueError("X must be a contiguous bfloat16 or float32 CUDA tensor")
+    _matrix(out, "out", X.dtype, X.shape, X.device)
+    with torch.cuda.device(X.device):
+        d = _dropout(p, rng, X.device)
+        out = out if out is not None else torch.empty_like(X)
+        _check(lib.lora_dropout(_ptr(X), X.numel(), 0 if X.dtype == torch.bfloat16 else 1, ctypes.byref(d), _ptr(out),
+                                _stream()))
+    return out
+
+
+def qlora_linear_dropout_fwd_workspace_bytes(M: int, d_out: int, d_in: int, r: int) -> int:
+    return int(lib.qlora_linear_dropout_fwd_workspace_bytes(M, d_out, d_in, r))
+
+
+def qlora_linear_dropout_bwd_workspace_bytes(M: int, d_out: int, d_in: int, r: int) -> int:
+    return int(lib.qlora_linear_dropout_bwd_workspace_bytes(M, d_out, d_in, r))
+
+
+def qlora_grouped_fwd_workspace_bytes(M: int, n_experts: int, d_out: int, d_in: int, r: int) -> int:
+    return int(lib.qlora_grouped_fwd_workspace_bytes(M, n_experts, d_out, d_in, r))
+
+
+def qlora_grouped_bwd_workspace_bytes(M: int, n_experts: int, d_out: int, d_in: int, r: int) -> int:
+    return int(lib.qlora_grouped_bwd_workspace_bytes(M, n_experts, d_out, d_in, r))
+
+
+def _group_shapes(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, lead: Tuple[int, ...]) -> Tuple[int, int]:
+    """(d_out of one expert, r) of an adapter whose tensors have the leading
+    dimensions `lead`; everything on the weight's device."""
+    dev = w.buffer.device
+    d_out = w.d_out // (lead[0] if lead else 1)
+    r = A.shape[-2] if A.dim() == 2 + len(lead) else 0
+    _matrix(A, "A", torch.bfloat16, lead + (r, w.d_in), dev)
+    _matrix(B, "B", torch.bfloat16, lead + (d_out, r), dev)
+    return d_out, r
+
+
+def _group_fwd(call, w, A, B, lead, X, p, rng, save_t, Y, workspace, T, need):
+    dev = w.buffer.device
+    d_out, r = _group_shapes(w, A, B, lead)
+    M = X.shape[0]
+    _matrix(X, "X", torch.bfloat16, (M, w.d_in), dev)
+    _matrix(Y, "Y", torch.bfloat16, (M, d_out), dev)
+    _matrix(T, "T", torch.float32, (M, r), dev)
+    with torch.cuda.device(dev):
+        Y = Y if Y is not None else torch.empty((M, d_out), dtype=torch.bfloat16, device=dev)
+        if not save_t:
+            T = None
+        elif T is None:
+            T = torch.empty((M, r), dtype=torch.float32, device=dev)
+        d = _dropout(p, rng, dev)
+        ws = workspace if workspace is not None else _workspace(need(M, *lead, d_out, w.d_in, r), dev)
+        _check(call(r, ctypes.byref(d), M, Y, T, ws))
+    return Y, T
+
+
+def _group_bwd(call, w, A, B, lead, X, T, dY, p, rng, need_dx, need_da, need_db, dA, dB, accumulate, dX, workspace,
+               need):
+    dev = w.buffer.device
+    d_out, r = _group_shapes(w, A, B, lead)
+    M = dY.shape[0]
+    _matrix(dY, "dY", torch.bfloat16, (M, d_out), dev)
+    _matrix(X, "X", torch.bfloat16, (M, w.d_in), dev)
+    _matrix(T, "T", torch.float32, (M, r), dev)
+    _matrix(dX, "dX", torch.bfloat16, (M, w.d_in), dev)
+    _matrix(dA, "dA", torch.bfloat16, A.shape, dev)
+    _matrix(dB, "dB", torch.bfloat16, B.shape, dev)
+    if accumulate and ((need_da and dA is None) or (need_db and dB is None)):
+        raise ValueError("accumulate needs the dA and dB to add to")
+    with torch.cuda.device(dev):
+        dX = (dX if dX is not None else torch.empty((M, w.d_in), dtype=torch.bfloat16, device=dev)) if need_dx else None
+        dA = (dA if dA is not None else torch.empty_like(A)) if need_da else None
+        dB = (dB if dB is not None else torch.empty_like(B)) if need_db else None
+        d = _dropout(p, rng, dev)
+        ws = workspace if workspace is not None else _workspace(need(M, *lead, d_out, w.d_in, r), dev)
+        _check(call(r, ctypes.byref(d), M, dX, dA, dB, 1 if accumulate else 0, ws))
+    return dX, dA, dB
+
+
+def _ws(ws: Optional[torch.Tensor]):
+    return _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def qlora_linear_dropout_fwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, scaling: float, X: torch.Tensor,
+                             p: float, rng: Optional[torch.Tensor], save_t: bool = True,
+                             Y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                             T: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Y = X W_hat^T + s (D A^T) B^T with D = keep .* X / (1 - p): the layer
+    with dropout on the adapter's input.  p and rng as for lora_dropout, which
+    drops the same elements of X.  Returns (Y, T), T = s D A^T in fp32."""
+    def call(r, d, M, Y, T, ws):
+        return lib.qlora_linear_dropout_fwd(ctypes.byref(w.struct), _ptr(A), _ptr(B), r, scaling, d, _ptr(X), M,
+                                            _ptr(Y), _ptr(T), *_ws(ws), _stream())
+    return _group_fwd(call, w, A, B, (), X, p, rng, save_t, Y, workspace, T, qlora_linear_dropout_fwd_workspace_bytes)
+
+
+def qlora_linear_dropout_bwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, scaling: float,
+                             X: Optional[torch.Tensor], T: Optional[torch.Tensor], dY: torch.Tensor, p: float,
+                             rng: Optional[torch.Tensor], need_dx: bool = True, need_da: bool = True,
+                             need_db: bool = True, dA: Optional[torch.Tensor] = None,
+                             dB: Optional[torch.Tensor] = None, accumulate: bool = False,
+                             dX: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """(dX, dA, dB) of qlora_linear_dropout_fwd called with the same p and the
+    same state in rng; the other arguments as for qlora_linear_bwd."""
+    def call(r, d, M, dX, dA, dB, acc, ws):
+        return lib.qlora_linear_dropout_bwd(ctypes.byref(w.struct), _ptr(A), _ptr(B), r, scaling, d, _ptr(X), _ptr(T),
+                                            _ptr(dY), M, _ptr(dX), _ptr(dA), _ptr(dB), acc, *_ws(ws), _stream())
+    return _group_bwd(call, w, A, B, (), X, T, dY, p, rng, need_dx, need_da, need_db, dA, dB, accumulate, dX, workspace,
+                      qlora_linear_dropout_bwd_workspace_bytes)
+
+
+def _experts(w: NF4Tensor, A: torch.Tensor, offsets: torch.Tensor) -> int:
+    if A.dim() != 3 or A.shape[0] < 1 or w.d_out % A.shape[0] != 0:
+        raise ValueError("A must be [n_experts, r, d_in], and the weight's %d rows n_experts times d_out" % w.d_out)
+    _matrix(offsets, "offsets", torch.int32, (A.shape[0] + 1,), w.buffer.device)
+    return A.shape[0]
+
+
+def qlora_grouped_fwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, scaling: float, X: torch.Tensor,
+                      offsets: torch.Tensor, p: float = 0.0, rng: Optional[torch.Tensor] = None, save_t: bool = True,
+                      Y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                      T: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The layer of a mixture of experts: w holds the stacked weights
+    [n_experts * d_out, d_in], A is [n_experts, r, d_in], B [n_experts, d_out,
+    r], and the rows offsets[e] .. offsets[e + 1] - 1 of X [M, d_in] go through
+    expert e (offsets: CUDA int32 [n_experts + 1], not decreasing).  Returns
+    (Y, T); rows outside the groups keep what Y and T held, which is nothing in
+    particular where they are allocated here.  p and rng: dropout on the
+    adapter's input, as for qlora_linear_dropout_fwd."""
+    e = _experts(w, A, offsets)
+
+    def call(r, d, M, Y, T, ws):
+        return lib.qlora_grouped_fwd(ctypes.byref(w.struct), e, _ptr(A), _ptr(B), r, scaling, d, _ptr(X), M,
+                                     _ptr(offsets), _ptr(Y), _ptr(T), *_ws(ws), _stream())
+    return _group_fwd(call, w, A, B, (e,), X, p, rng, save_t, Y, workspace, T, qlora_grouped_fwd_workspace_bytes)
+
+
+def qlora_grouped_bwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, scaling: float, X: Optional[torch.Tensor],
+                      T: Optional[torch.Tensor], dY: torch.Tensor, offsets: torch.Tensor, p: float = 0.0,
+                      rng: Optional[torch.Tensor] = None, need_dx: bool = True, need_da: bool = True,
+                      need_db: bool = True, dA: Optional[torch.Tensor] = None, dB: Optional[torch.Tensor] = None,
+                      accumulate: bool = False, dX: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None):
+    """(dX, dA, dB) of qlora_grouped_fwd called with the same offsets, p and
+    state in rng; dA [n_experts, r, d_in] and dB [n_experts, d_out, r] are zero
+    for an expert without rows.  The other arguments as for qlora_linear_bwd."""
+    e = _experts(w, A, offsets)
+
+    def call(r, d, M, dX, dA, dB, acc, ws):
+        return lib.qlora_grouped_bwd(ctypes.byref(w.struct), e, _ptr(A), _ptr(B), r, scaling, d, _ptr(X), _ptr(T),
+                                     _ptr(dY), M, _ptr(offsets), _ptr(dX), _ptr(dA), _ptr(dB), acc, *_ws(ws),
+                                     _stream())
+    return _group_bwd(call, w, A, B, (e,), X, T, dY, p, rng, need_dx, need_da, need_db, dA, dB, accumulate, dX,
+                      workspace, qlora_grouped_bwd_workspace_bytes)
 
 
 def nf4_merge_workspace_bytes(d_out: int, d_in: int) -> int:

@@ -8,6 +8,7 @@
 #include <string>
 
 #include "nf4lora.h"
+#include "adapter.h"
 #include "common.cuh"
 #include "kernels.h"
 #include "layer.h"
@@ -98,6 +99,24 @@ int check_layer_common(const nf4_tensor* w, const uint16_t* A, const uint16_t* B
     if (M < 0 || M >= (int64_t(1) << 31)) return fail(NF4_ERR_INVALID_ARG, "M = %lld outside [0, 2^31)", (long long)M);
     if (!A || !B) return fail(NF4_ERR_INVALID_ARG, "A or B is NULL");
     if (!aligned16(A) || !aligned16(B)) return fail(NF4_ERR_MISALIGNED, "A or B not 16-byte aligned");
+    return NF4_OK;
+}
+
+// Host side of a lora_dropout_params: NULL or p = 0 drops nothing.
+int check_dropout(const lora_dropout_params* d, DropArgs* out) {
+    *out = DropArgs{nullptr, 0u, 1.0f};
+    if (d == nullptr) return NF4_OK;
+    if (!(d->p >= 0.0 && d->p < 1.0)) return fail(NF4_ERR_INVALID_ARG, "dropout p = %g outside [0, 1)", d->p);
+    const double t = std::floor(d->p * 32768.0 + 0.5);
+    if (t >= 32768.0)
+        return fail(NF4_ERR_INVALID_ARG, "dropout p = %g rounds to 1 in steps of 2^-15: nothing would be kept", d->p);
+    if (t == 0.0) return NF4_OK;
+    if (d->state == nullptr) return fail(NF4_ERR_INVALID_ARG, "dropout state is NULL with p = %g", d->p);
+    if (reinterpret_cast<uintptr_t>(d->state) & 7u)
+        return fail(NF4_ERR_MISALIGNED, "dropout state not 8-byte aligned");
+    out->rng = d->state;
+    out->threshold = static_cast<uint32_t>(t);
+    out->gain = static_cast<float>(32768.0 / (32768.0 - t));
     return NF4_OK;
 }
 
@@ -289,6 +308,175 @@ int qlora_linear_bwd(const nf4_tensor* w, const uint16_t* A, const uint16_t* B, 
     return ok();
 }
 
+// ------------------------------------------------------------------ dropout, experts
+int lora_dropout(const void* X, int64_t n, int dtype, const lora_dropout_params* dropout, void* out, void* stream) {
+    if (n < 0) return fail(NF4_ERR_INVALID_ARG, "n = %lld < 0", (long long)n);
+    if (dtype != NF4_DTYPE_BF16 && dtype != NF4_DTYPE_F32) return fail(NF4_ERR_INVALID_ARG, "dtype %d unknown", dtype);
+    if (dropout == nullptr) return fail(NF4_ERR_INVALID_ARG, "dropout is NULL");
+    DropArgs drop;
+    int rc = check_dropout(dropout, &drop);
+    if (rc) return rc;
+    if (n == 0) return ok();
+    if (!X || !out) return fail(NF4_ERR_INVALID_ARG, "X or out is NULL");
+    if (!aligned16(X) || !aligned16(out)) return fail(NF4_ERR_MISALIGNED, "X or out not 16-byte aligned");
+    int sms = 0;
+    rc = check_device(&sms);
+    if (rc) return rc;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (drop.threshold != 0) {
+        e = launch_lora_dropout(X, n, dtype == NF4_DTYPE_BF16, drop, out, sms, st);
+    } else if (X != out) {
+        const size_t bytes = static_cast<size_t>(n) * (dtype == NF4_DTYPE_BF16 ? 2 : 4);
+        e = cudaMemcpyAsync(out, X, bytes, cudaMemcpyDeviceToDevice, st);
+    }
+    if (e != cudaSuccess) return fail(NF4_ERR_CUDA, "lora_dropout launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+static bool valid_group_shape(int64_t M, int n_experts, int64_t d_out, int64_t d_in, int r) {
+    return valid_weight_shape(d_out, d_in) && M >= 1 && M < (int64_t(1) << 31) && r >= 1 && r <= 256 &&
+           n_experts >= 1 && n_experts <= NF4_MAX_EXPERTS && d_out * n_experts < (int64_t(1) << 31);
+}
+
+size_t qlora_linear_dropout_fwd_workspace_bytes(int64_t M, int64_t d_out, int64_t d_in, int r) {
+    return qlora_grouped_fwd_workspace_bytes(M, 1, d_out, d_in, r);
+}
+
+size_t qlora_linear_dropout_bwd_workspace_bytes(int64_t M, int64_t d_out, int64_t d_in, int r) {
+    return qlora_grouped_bwd_workspace_bytes(M, 1, d_out, d_in, r);
+}
+
+size_t qlora_grouped_fwd_workspace_bytes(int64_t M, int n_experts, int64_t d_out, int64_t d_in, int r) {
+    if (!valid_group_shape(M, n_experts, d_out, d_in, r)) return 0;
+    return static_cast<size_t>(group_fwd_workspace_bytes(M, n_experts, d_out, d_in, r, kPlanSMs));
+}
+
+size_t qlora_grouped_bwd_workspace_bytes(int64_t M, int n_experts, int64_t d_out, int64_t d_in, int r) {
+    if (!valid_group_shape(M, n_experts, d_out, d_in, r)) return 0;
+    return static_cast<size_t>(group_bwd_workspace_bytes(M, n_experts, d_out, d_in, r, kPlanSMs));
+}
+
+// The checks that the dense and the grouped calls share; fills the context
+// (without its stream).  Grouped calls have offsets, dense ones have not.
+static int check_group(const nf4_tensor* w, int n_experts, bool grouped, const int32_t* offsets, const uint16_t* A,
+                       const uint16_t* B, int r, float scaling, const lora_dropout_params* dropout, int64_t M,
+                       GroupCtx* c) {
+    int rc = check_tensor(w);
+    if (rc) return rc;
+    if (n_experts < 1 || n_experts > NF4_MAX_EXPERTS)
+        return fail(NF4_ERR_INVALID_ARG, "n_experts = %d outside [1, %d]", n_experts, NF4_MAX_EXPERTS);
+    if (w->d_out % n_experts != 0)
+        return fail(NF4_ERR_UNSUPPORTED_SHAPE, "%lld weight rows do not divide into %d experts", (long long)w->d_out,
+                    n_experts);
+    if (w->d_out / n_experts % 8 != 0)
+        return fail(NF4_ERR_UNSUPPORTED_SHAPE, "d_out = %lld must be a multiple of 8",
+                    (long long)(w->d_out / n_experts));
+    rc = check_layer_common(w, A, B, r, scaling, M);
+    if (rc) return rc;
+    DropArgs drop;
+    rc = check_dropout(dropout, &drop);
+    if (rc) return rc;
+    if (grouped && M > 0) {
+        if (offsets == nullptr) return fail(NF4_ERR_INVALID_ARG, "offsets is NULL");
+        if (reinterpret_cast<uintptr_t>(offsets) & 3u) return fail(NF4_ERR_MISALIGNED, "offsets not 4-byte aligned");
+    }
+    *c = GroupCtx{w->codes, w->qscale, w->scale2, w->scale_mean, w->absmax, n_experts, w->d_out / n_experts,
+                  w->d_in, M, grouped ? offsets : nullptr, r, scaling, drop, kPlanSMs, nullptr};
+    return NF4_OK;
+}
+
+static int run_fwd(const char* name, GroupCtx& c, const uint16_t* A, const uint16_t* B, const uint16_t* X, uint16_t* Y,
+                   float* T_saved, void* ws, size_t ws_bytes, void* stream) {
+    if (c.M == 0) return ok();  // an empty batch
+    if (!X || !Y) return fail(NF4_ERR_INVALID_ARG, "X or Y is NULL");
+    if (!aligned16(X) || !aligned16(Y) || (T_saved && !aligned16(T_saved)))
+        return fail(NF4_ERR_MISALIGNED, "X, Y or T_saved not 16-byte aligned");
+    int rc = check_ws(ws, ws_bytes, group_fwd_workspace_bytes(c.M, c.E, c.N, c.K, c.r, kPlanSMs));
+    if (rc) return rc;
+    int sms = 0;
+    rc = check_device(&sms);
+    if (rc) return rc;
+    c.stream = static_cast<cudaStream_t>(stream);
+    rc = group_fwd(c, A, B, X, Y, T_saved, static_cast<uint8_t*>(ws));
+    if (rc == -1) return fail(NF4_ERR_CUDA, "%s: tensor map encoding failed", name);
+    if (rc) return fail(NF4_ERR_CUDA, "%s launch: %s", name, cudaGetErrorString(group_last_cuda_error()));
+    return ok();
+}
+
+static int run_bwd(const char* name, GroupCtx& c, const uint16_t* A, const uint16_t* B, const uint16_t* X,
+                   const float* T_saved, const uint16_t* dY, uint16_t* dX, uint16_t* dA, uint16_t* dB,
+                   int accumulate_grads, void* ws, size_t ws_bytes, void* stream) {
+    if (accumulate_grads != 0 && accumulate_grads != 1)
+        return fail(NF4_ERR_INVALID_ARG, "accumulate_grads must be 0 or 1");
+    if ((dX && !aligned16(dX)) || (dA && !aligned16(dA)) || (dB && !aligned16(dB)))
+        return fail(NF4_ERR_MISALIGNED, "dX, dA or dB not 16-byte aligned");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (c.M == 0) {
+        // an empty batch: zero gradients for the adapters, nothing else
+        if (accumulate_grads) return ok();
+        if (dA && cudaMemsetAsync(dA, 0, static_cast<size_t>(c.E) * c.r * c.K * 2, st) != cudaSuccess)
+            return fail(NF4_ERR_CUDA, "%s: clearing dA failed", name);
+        if (dB && cudaMemsetAsync(dB, 0, static_cast<size_t>(c.E) * c.N * c.r * 2, st) != cudaSuccess)
+            return fail(NF4_ERR_CUDA, "%s: clearing dB failed", name);
+        return ok();
+    }
+    if (!dY) return fail(NF4_ERR_INVALID_ARG, "dY is NULL");
+    const bool need_x = dA != nullptr || (dB != nullptr && T_saved == nullptr);
+    if (need_x && !X) return fail(NF4_ERR_INVALID_ARG, "X is NULL but dA, or dB without T_saved, is requested");
+    if (!aligned16(dY) || (X && !aligned16(X)) || (T_saved && !aligned16(T_saved)))
+        return fail(NF4_ERR_MISALIGNED, "an array argument is not 16-byte aligned");
+    if (!dX && !dA && !dB) return ok();
+    int rc = check_ws(ws, ws_bytes, group_bwd_workspace_bytes(c.M, c.E, c.N, c.K, c.r, kPlanSMs));
+    if (rc) return rc;
+    int sms = 0;
+    rc = check_device(&sms);
+    if (rc) return rc;
+    c.stream = st;
+    rc = group_bwd(c, A, B, X, T_saved, dY, dX, dA, dB, accumulate_grads, static_cast<uint8_t*>(ws));
+    if (rc == -1) return fail(NF4_ERR_CUDA, "%s: tensor map encoding failed", name);
+    if (rc) return fail(NF4_ERR_CUDA, "%s launch: %s", name, cudaGetErrorString(group_last_cuda_error()));
+    return ok();
+}
+
+int qlora_linear_dropout_fwd(const nf4_tensor* w, const uint16_t* A, const uint16_t* B, int r, float scaling,
+                             const lora_dropout_params* dropout, const uint16_t* X, int64_t M, uint16_t* Y,
+                             float* T_saved, void* ws, size_t ws_bytes, void* stream) {
+    GroupCtx c;
+    const int rc = check_group(w, 1, false, nullptr, A, B, r, scaling, dropout, M, &c);
+    return rc ? rc : run_fwd("qlora_linear_dropout_fwd", c, A, B, X, Y, T_saved, ws, ws_bytes, stream);
+}
+
+int qlora_linear_dropout_bwd(const nf4_tensor* w, const uint16_t* A, const uint16_t* B, int r, float scaling,
+                             const lora_dropout_params* dropout, const uint16_t* X, const float* T_saved,
+                             const uint16_t* dY, int64_t M, uint16_t* dX, uint16_t* dA, uint16_t* dB,
+                             int accumulate_grads, void* ws, size_t ws_bytes, void* stream) {
+    GroupCtx c;
+    const int rc = check_group(w, 1, false, nullptr, A, B, r, scaling, dropout, M, &c);
+    return rc ? rc
+              : run_bwd("qlora_linear_dropout_bwd", c, A, B, X, T_saved, dY, dX, dA, dB, accumulate_grads, ws,
+                        ws_bytes, stream);
+}
+
+int qlora_grouped_fwd(const nf4_tensor* w, int n_experts, const uint16_t* A, const uint16_t* B, int r, float scaling,
+                      const lora_dropout_params* dropout, const uint16_t* X, int64_t M, const int32_t* offsets,
+                      uint16_t* Y, float* T_saved, void* ws, size_t ws_bytes, void* stream) {
+    GroupCtx c;
+    const int rc = check_group(w, n_experts, true, offsets, A, B, r, scaling, dropout, M, &c);
+    return rc ? rc : run_fwd("qlora_grouped_fwd", c, A, B, X, Y, T_saved, ws, ws_bytes, stream);
+}
+
+int qlora_grouped_bwd(const nf4_tensor* w, int n_experts, const uint16_t* A, const uint16_t* B, int r, float scaling,
+                      const lora_dropout_params* dropout, const uint16_t* X, const float* T_saved,
+                      const uint16_t* dY, int64_t M, const int32_t* offsets, uint16_t* dX, uint16_t* dA, uint16_t* dB,
+                      int accumulate_grads, void* ws, size_t ws_bytes, void* stream) {
+    GroupCtx c;
+    const int rc = check_group(w, n_experts, true, offsets, A, B, r, scaling, dropout, M, &c);
+    return rc ? rc
+              : run_bwd("qlora_grouped_bwd", c, A, B, X, T_saved, dY, dX, dA, dB, accumulate_grads, ws, ws_bytes,
+                        stream);
+}
+
 const char* nf4lora_last_error_string(void) { return t_last_error.c_str(); }
 
 size_t nf4_merge_workspace_bytes(int64_t d_out, int64_t d_in) {
@@ -410,6 +598,8 @@ int nf4lora_device_status(void* stream) {
     if (cudaMemcpyFromSymbol(&v, g_device_status, sizeof(int)) != cudaSuccess ||
         cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int)) != cudaSuccess)
         return fail(NF4_ERR_CUDA, "status word access failed");
+    if (v == kStatusOffsets)
+        return fail(NF4_ERR_INVALID_ARG, "group offsets out of order or outside [0, M]: the call's results are undefined");
     if (v != 0) return fail(NF4_ERR_TIMEOUT, "a kernel abandoned a bounded wait (status %d)", v);
     return ok();
 }

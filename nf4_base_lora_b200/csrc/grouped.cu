@@ -1,0 +1,432 @@
+// Host orchestration of the NF4-LoRA layer with adapter dropout and of the
+// layer of a mixture of experts (kernels: grouped.cuh, rank.cuh; formulas
+// there).  Both are the same chain; the dense layer is one group of all rows.
+//
+//   forward   rank T -> sum (pair of T) -> fused product
+//   backward  rank V -> sum (pair of V) -> fused input gradient
+//             -> pair of the saved T -> dB -> dA
+//
+// Every kernel is a programmatic dependent of the one before it and waits for
+// it first, except the fused products, which wait only before they read the
+// pair: what else they read was complete before the sum started.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "adapter.h"
+#include "grouped.cuh"
+#include "kernels.h"
+#include "rank.cuh"
+#include "trace.h"
+
+namespace nf4lora {
+
+namespace {
+
+thread_local cudaError_t t_error = cudaSuccess;
+cudaError_t keep(cudaError_t e) {
+    if (e != cudaSuccess) t_error = e;
+    return e;
+}
+
+int64_t up256(int64_t b) { return (b + 255) & ~int64_t(255); }
+int64_t ceil_to(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ------------------------------------------------------------------ tensor maps
+// [experts][rows][inner] with rows `ld` bytes apart and experts `rows` rows
+// apart (experts 0: a plain matrix).  Reads outside give zeros.
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, const void* ptr, int64_t inner, int64_t rows,
+              int64_t experts, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    if (!fn) return false;
+    const int rank = experts > 0 ? 3 : 2;
+    const cuuint64_t ld = static_cast<cuuint64_t>(inner) * elem_bytes;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(experts)};
+    cuuint64_t strides[2] = {ld, ld * static_cast<cuuint64_t>(rows)};
+    cuuint32_t box[3] = {box_inner, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, type, rank, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool map16(CUtensorMap* m, const void* ptr, int64_t inner, int64_t rows, int64_t experts, uint32_t box_rows) {
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, inner, rows, experts, 64, box_rows,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool map_packed(CUtensorMap* m, const uint8_t* codes, int64_t N, int64_t K, int64_t experts, uint32_t box_inner,
+                uint32_t box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE) {
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, K / 2, N, experts, box_inner, box_rows, swizzle);
+}
+
+// ------------------------------------------------------------------ launches
+// Opt-in to `smem` bytes of dynamic shared memory, once per kernel and device
+// (kept out of stream captures after the first call).
+cudaError_t opt_in(const void* kernel, int smem, bool (&done)[64]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    return e;
+}
+
+// A programmatic dependent of the kernel before it on the stream.
+template <typename Kern, typename... Args>
+cudaError_t launch_dependent(const char* name, Kern kern, dim3 grid, int threads, int smem, cudaStream_t st,
+                             const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    TraceScope trace(name, st);
+    return keep(cudaLaunchKernelEx(&cfg, kern, args...));
+}
+
+dim3 flat_grid(int64_t items, int num_sms) {
+    return dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(div_up(items, 256), num_sms * 8))));
+}
+
+// ------------------------------------------------------------------ sizes
+// Row tiles that any division of M rows into E groups can need.
+int64_t most_tiles(const int32_t* offsets, int E, int64_t M, int rows) {
+    if (offsets == nullptr) return div_up(M, rows);
+    return (M + (rows - 1) * std::min<int64_t>(E, M)) / rows;
+}
+
+// Row tiles to expect (for split sizes): half a tile lost per group.
+int64_t likely_tiles(int E, int64_t M, int rows) {
+    return std::max<int64_t>(1, (M + rows / 2 * std::min<int64_t>(E, M)) / rows);
+}
+
+struct Split {
+    int splits;
+    int per;
+};
+
+// `steps` split into parts of at least four steps so that tiles x parts is
+// about `ctas`; no part is empty.
+Split split_steps(int64_t tiles, int64_t steps, int ctas) {
+    int64_t s = std::max<int64_t>(1, ctas / std::max<int64_t>(1, tiles));
+    s = std::min(s, std::max<int64_t>(1, steps / 4));
+    const int64_t per = div_up(steps, s);
+    return {static_cast<int>(div_up(steps, per)), static_cast<int>(per)};
+}
+
+int rank_width(int r) { return static_cast<int>(ceil_to(r, 16)); }
+int rank64(int r) { return static_cast<int>(ceil_to(r, 64)); }
+
+// Contraction splits of T (steps over K) and V (over N), and the parts of a
+// group's rows of dB (out rows N) and dA (out rows K).
+Split rows_split(int E, int64_t M, int64_t contraction, int num_sms) {
+    return split_steps(likely_tiles(E, M, 128), div_up(contraction, 64), num_sms);
+}
+int grad_splits(int E, int64_t M, int64_t out_rows, int num_sms) {
+    const int64_t groups = std::min<int64_t>(E, M);
+    return split_steps(div_up(out_rows, 256) * groups, div_up(div_up(M, groups), 64), num_sms).splits;
+}
+
+struct Workspace {
+    uint16_t *T2, *V2, *B8;
+    float* part;
+    int64_t bytes;
+};
+
+Workspace layout(uint8_t* base, int64_t M, int E, int64_t N, int64_t K, int r, int num_sms, bool backward) {
+    Workspace w{};
+    int64_t off = 0;
+    auto take = [&](int64_t bytes) {
+        uint8_t* p = base ? base + off : nullptr;
+        off += up256(bytes);
+        return p;
+    };
+    const int64_t pair = M * 2 * rank64(r) * 2, rn = rank_width(r);
+    w.T2 = reinterpret_cast<uint16_t*>(take(pair));
+    if (backward) w.V2 = reinterpret_cast<uint16_t*>(take(pair));
+    if (r % 8 != 0) w.B8 = reinterpret_cast<uint16_t*>(take(E * N * ceil_to(r, 8) * 2));
+    int64_t part = rows_split(E, M, K, num_sms).splits * M * rn;
+    if (backward) {
+        part = std::max(part, rows_split(E, M, N, num_sms).splits * M * rn);
+        const int sb = grad_splits(E, M, N, num_sms), sa = grad_splits(E, M, K, num_sms);
+        if (sb > 1) part = std::max(part, sb * E * N * rn);
+        if (sa > 1) part = std::max(part, sa * E * K * rn);
+    }
+    w.part = reinterpret_cast<float*>(take(part * 4));
+    w.bytes = off;
+    return w;
+}
+
+// ------------------------------------------------------------------ rank-r products
+// B with its rows padded to a multiple of eight elements (16 bytes, as tensor
+// maps need).
+__global__ void k_pad_columns(const uint16_t* __restrict__ src, int64_t rows, int cols, int padded,
+                              uint16_t* __restrict__ dst) {
+    grid_dependency_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t total = rows * padded;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t row = i / padded;
+        const int c = static_cast<int>(i - row * padded);
+        dst[i] = c < cols ? src[row * cols + c] : uint16_t(0);
+    }
+}
+
+template <int MODE, bool DROP>
+cudaError_t launch_rank(const char* name, const CUtensorMap& a, const CUtensorMap& b, RankArgs g, dim3 grid,
+                        cudaStream_t st) {
+    constexpr bool tok = MODE == RANK_DB || MODE == RANK_DA;
+    const int rchunks = (g.rn + 63) / 64;
+    g.a_bytes = tok ? 4 * 8192 : 16384;
+    g.b_bytes = tok ? 2 * rchunks * 8192 : MODE == RANK_V ? rchunks * 8192 : g.rn * 128;
+    const int slot = g.a_bytes + g.b_bytes;
+    // three stages or more of half an SM's shared memory, so that two CTAs
+    // overlap their ends; else what one CTA can have
+    int stages = std::min(kRankStages, 110 * 1024 / slot);
+    if (stages < 3) stages = std::min(kRankStages, 224 * 1024 / slot);
+    g.stages = stages;
+    const int cols = tok ? 2 * g.rn : g.rn;
+    g.tmem_cols = 32;
+    while (g.tmem_cols < cols) g.tmem_cols *= 2;
+    static bool done[64] = {};
+    const cudaError_t e = opt_in(reinterpret_cast<const void*>(&k_rank<MODE, DROP>), 226 * 1024, done);
+    if (e != cudaSuccess) return keep(e);
+    return launch_dependent(name, k_rank<MODE, DROP>, grid, kRankThreads, stages * slot + 1024, st, a, b, g);
+}
+
+RankArgs rank_args(const GroupCtx& c) {
+    RankArgs g{};
+    g.offsets = c.offsets;
+    g.E = c.E;
+    g.M = static_cast<int>(c.M);
+    g.r = c.r;
+    g.rn = rank_width(c.r);
+    g.r64 = rank64(c.r);
+    g.drop = c.drop;
+    g.drop_cols = static_cast<int>(c.K);
+    return g;
+}
+
+// The pair of T (act X, factor A) or V (act dY, factor B): the product in
+// splits, then their sum.
+int rank_rows(const GroupCtx& c, bool is_t, const uint16_t* act, const uint16_t* factor, uint16_t* pair, float* out32,
+              float* part) {
+    const int64_t contraction = is_t ? c.K : c.N;
+    const Split sp = rows_split(c.E, c.M, contraction, c.num_sms);
+    RankArgs g = rank_args(c);
+    g.k_steps = static_cast<int>(div_up(contraction, 64));
+    g.k_per_split = sp.per;
+    g.part = part;
+    g.part_slice = c.M * g.rn;
+    CUtensorMap ma, mb;
+    std::memset(&ma, 0, sizeof(ma));
+    std::memset(&mb, 0, sizeof(mb));
+    if (!map16(&ma, act, contraction, c.M, 0, 128)) return -1;
+    if (is_t ? !map16(&mb, factor, c.K, c.r, c.E, g.rn) : !map16(&mb, factor, ceil_to(c.r, 8), c.N, c.E, 64)) return -1;
+    const dim3 grid(static_cast<unsigned>(most_tiles(c.offsets, c.E, c.M, 128)), 1, sp.splits);
+    const bool drop = is_t && c.drop.threshold != 0;
+    const cudaError_t e = drop   ? launch_rank<RANK_T, true>("rank_t_drop", ma, mb, g, grid, c.stream)
+                          : is_t ? launch_rank<RANK_T, false>("rank_t", ma, mb, g, grid, c.stream)
+                                 : launch_rank<RANK_V, false>("rank_v", ma, mb, g, grid, c.stream);
+    if (e != cudaSuccess) return -2;
+    RankRowsSumArgs s{};
+    s.offsets = c.offsets;
+    s.E = c.E;
+    s.M = g.M;
+    s.part = part;
+    s.splits = sp.splits;
+    s.slice = g.part_slice;
+    s.r = c.r;
+    s.rn = g.rn;
+    s.r64 = g.r64;
+    s.alpha = drop ? c.s * c.drop.gain : c.s;
+    s.pair = pair;
+    s.out32 = out32;
+    s.check = 1;
+    return launch_dependent("rank_sum", k_rank_rows_sum, flat_grid(c.M * (g.r64 / 4), c.num_sms), 256, 0, c.stream,
+                            s) == cudaSuccess ? 0 : -2;
+}
+
+// dB (act dY, pair T2) or dA (act X, pair V2).
+int rank_grad(const GroupCtx& c, bool is_b, const uint16_t* act, const uint16_t* pair, uint16_t* out, int accumulate,
+              float* part) {
+    const int64_t rows = is_b ? c.N : c.K;
+    const int splits = grad_splits(c.E, c.M, rows, c.num_sms);
+    const bool drop = !is_b && c.drop.threshold != 0;
+    RankArgs g = rank_args(c);
+    g.rows = static_cast<int>(rows);
+    g.splits = splits;
+    g.alpha = drop ? c.drop.gain : 1.0f;
+    g.part = part;
+    g.part_slice = int64_t(c.E) * rows * g.rn;
+    g.out = splits == 1 ? out : nullptr;
+    g.accumulate = accumulate;
+    CUtensorMap ma, mb;
+    std::memset(&ma, 0, sizeof(ma));
+    std::memset(&mb, 0, sizeof(mb));
+    if (!map16(&ma, act, rows, c.M, 0, 64) || !map16(&mb, pair, 2 * g.r64, c.M, 0, 64)) return -1;
+    const dim3 grid(static_cast<unsigned>(div_up(rows, 256)), static_cast<unsigned>(c.E), splits);
+    const cudaError_t e = is_b   ? launch_rank<RANK_DB, false>("rank_db", ma, mb, g, grid, c.stream)
+                          : drop ? launch_rank<RANK_DA, true>("rank_da_drop", ma, mb, g, grid, c.stream)
+                                 : launch_rank<RANK_DA, false>("rank_da", ma, mb, g, grid, c.stream);
+    if (e != cudaSuccess) return -2;
+    if (splits == 1) return 0;
+    const dim3 sum_grid = flat_grid(int64_t(c.E) * rows * c.r, c.num_sms);
+    auto sum = [&](auto kern) {
+        return launch_dependent("rank_grad_sum", kern, sum_grid, 256, 0, c.stream, static_cast<const float*>(part),
+                                splits, g.part_slice, static_cast<int64_t>(c.E), static_cast<int>(rows), c.r, g.rn,
+                                g.alpha, out, accumulate);
+    };
+    return (is_b ? sum(k_rank_grad_sum<false>) : sum(k_rank_grad_sum<true>)) == cudaSuccess ? 0 : -2;
+}
+
+// ------------------------------------------------------------------ fused products
+template <bool DX, int MSUB, bool DROP>
+cudaError_t launch_group_gemm(const char* name, const CUtensorMap* m, const GroupGemmArgs& g, dim3 grid,
+                              cudaStream_t st) {
+    using C = GroupGemmConfig<DX, MSUB>;
+    static bool done[64] = {};
+    const cudaError_t e = opt_in(reinterpret_cast<const void*>(&k_group_gemm<DX, MSUB, DROP>), C::kSmem, done);
+    if (e != cudaSuccess) return keep(e);
+    return launch_dependent(name, k_group_gemm<DX, MSUB, DROP>, grid, C::kThreads, C::kSmem, st, m[0], m[1], m[2],
+                            m[3], g);
+}
+
+// Y (act X, pair T2, factor B) or dX (act dY, pair V2, factor A).
+int fused(const GroupCtx& c, bool dx, const uint16_t* act, const uint16_t* pair, const uint16_t* factor,
+          uint16_t* out) {
+    const int64_t contraction = dx ? c.N : c.K, cols = dx ? c.K : c.N;
+    const int r64 = rank64(c.r);
+    GroupGemmArgs g{};
+    g.offsets = c.offsets;
+    g.E = c.E;
+    g.M = static_cast<int>(c.M);
+    g.cols = static_cast<int>(cols);
+    g.k_main = static_cast<int>(div_up(contraction, 64));
+    g.k_ext = 2 * r64 / 64;
+    g.qscale = c.qscale;
+    g.scale2 = c.scale2;
+    g.scale_mean = c.scale_mean;
+    g.absmax = c.absmax;
+    g.w_rows = static_cast<int>(c.N);
+    g.w_blocks_per_row = static_cast<int>(c.K / 64);
+    g.out = out;
+    g.drop = c.drop;
+    CUtensorMap m[4];
+    std::memset(m, 0, sizeof(m));
+    if (!map16(&m[0], act, contraction, c.M, 0, 128) || !map16(&m[2], pair, 2 * r64, c.M, 0, 128)) return -1;
+    if (dx ? !map_packed(&m[1], c.codes, c.N, c.K, c.E, 128, 64) || !map16(&m[3], factor, c.K, c.r, c.E, 64)
+           : !map_packed(&m[1], c.codes, c.N, c.K, c.E, 32, 256) ||
+                 !map16(&m[3], factor, ceil_to(c.r, 8), c.N, c.E, 256))
+        return -1;
+    const int64_t col_tiles = div_up(cols, 256);
+    // 256-row tiles halve the decode per MMA; they need enough tiles for every
+    // SM and groups of more than 128 rows
+    const bool wide = likely_tiles(c.E, c.M, 256) * col_tiles >= c.num_sms && c.M > 128 * int64_t(c.E);
+    const int64_t row_tiles = most_tiles(c.offsets, c.E, c.M, wide ? 256 : 128);
+    // The tiles that run together share what they re-read.  Column tiles
+    // fastest reads the activations once and a group's weight once per row
+    // tile of that group, from L2 where the weight fits it; one dense weight
+    // that does not goes row tiles fastest unless the activations are larger.
+    g.cols_fastest = (c.offsets != nullptr || 2 * c.M * contraction > c.N * c.K * 33 / 64) && row_tiles <= 65535;
+    const dim3 grid = g.cols_fastest ? dim3(static_cast<unsigned>(col_tiles), static_cast<unsigned>(row_tiles))
+                                     : dim3(static_cast<unsigned>(row_tiles), static_cast<unsigned>(col_tiles));
+    const bool drop = dx && c.drop.threshold != 0;
+    cudaError_t e;
+    if (!dx)
+        e = wide ? launch_group_gemm<false, 2, false>("group_gemm_fwd", m, g, grid, c.stream)
+                 : launch_group_gemm<false, 1, false>("group_gemm_fwd", m, g, grid, c.stream);
+    else if (drop)
+        e = wide ? launch_group_gemm<true, 2, true>("group_gemm_dx_drop", m, g, grid, c.stream)
+                 : launch_group_gemm<true, 1, true>("group_gemm_dx_drop", m, g, grid, c.stream);
+    else
+        e = wide ? launch_group_gemm<true, 2, false>("group_gemm_dx", m, g, grid, c.stream)
+                 : launch_group_gemm<true, 1, false>("group_gemm_dx", m, g, grid, c.stream);
+    return e == cudaSuccess ? 0 : -2;
+}
+
+// B as the tensor maps can read it: itself, or its padded copy.
+int padded_b(const GroupCtx& c, const uint16_t*& B, uint16_t* B8) {
+    if (B8 == nullptr) return 0;
+    const int r8 = static_cast<int>(ceil_to(c.r, 8));
+    const int64_t rows = int64_t(c.E) * c.N;
+    if (launch_dependent("pad_b", k_pad_columns, flat_grid(rows * r8, c.num_sms), 256, 0, c.stream, B, rows, c.r, r8,
+                         B8) != cudaSuccess)
+        return -2;
+    B = B8;
+    return 0;
+}
+
+}  // namespace
+
+cudaError_t group_last_cuda_error() {
+    const cudaError_t e = t_error;
+    t_error = cudaSuccess;
+    return e;
+}
+
+int64_t group_fwd_workspace_bytes(int64_t M, int E, int64_t N, int64_t K, int r, int num_sms) {
+    return layout(nullptr, M, E, N, K, r, num_sms, false).bytes;
+}
+int64_t group_bwd_workspace_bytes(int64_t M, int E, int64_t N, int64_t K, int r, int num_sms) {
+    return layout(nullptr, M, E, N, K, r, num_sms, true).bytes;
+}
+
+int group_fwd(const GroupCtx& c, const uint16_t* A, const uint16_t* B, const uint16_t* X, uint16_t* Y, float* T_saved,
+              uint8_t* ws) {
+    const Workspace w = layout(ws, c.M, c.E, c.N, c.K, c.r, c.num_sms, false);
+    int rc = padded_b(c, B, w.B8);
+    if (rc == 0) rc = rank_rows(c, true, X, A, w.T2, T_saved, w.part);
+    if (rc == 0) rc = fused(c, false, X, w.T2, B, Y);
+    return rc;
+}
+
+int group_bwd(const GroupCtx& c, const uint16_t* A, const uint16_t* B, const uint16_t* X, const float* T_saved,
+              const uint16_t* dY, uint16_t* dX, uint16_t* dA, uint16_t* dB, int accumulate, uint8_t* ws) {
+    const Workspace w = layout(ws, c.M, c.E, c.N, c.K, c.r, c.num_sms, true);
+    int rc = 0;
+    if (dX != nullptr || dA != nullptr) {
+        rc = padded_b(c, B, w.B8);
+        if (rc == 0) rc = rank_rows(c, false, dY, B, w.V2, nullptr, w.part);
+    }
+    if (rc == 0 && dX != nullptr) rc = fused(c, true, dY, w.V2, A, dX);
+    if (rc == 0 && dB != nullptr) {
+        if (T_saved == nullptr) {
+            rc = rank_rows(c, true, X, A, w.T2, nullptr, w.part);
+        } else {
+            const int r64 = rank64(c.r);
+            if (launch_dependent("rank_pair", k_rank_pair, flat_grid(c.M * r64, c.num_sms), 256, 0, c.stream, T_saved,
+                                 c.M, c.r, r64, w.T2) != cudaSuccess)
+                rc = -2;
+        }
+        if (rc == 0) rc = rank_grad(c, true, dY, w.T2, dB, accumulate, w.part);
+    }
+    if (rc == 0 && dA != nullptr) rc = rank_grad(c, false, X, w.V2, dA, accumulate, w.part);
+    return rc;
+}
+
+}  // namespace nf4lora
