@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "adapter.h"
 #include "grouped.cuh"
@@ -89,22 +90,33 @@ cudaError_t opt_in(const void* kernel, int smem, bool (&done)[64]) {
     return e;
 }
 
-// A programmatic dependent of the kernel before it on the stream.
+// A programmatic dependent of the kernel before it on the stream, in clusters
+// of `cluster` CTAs along grid.x.
 template <typename Kern, typename... Args>
-cudaError_t launch_dependent(const char* name, Kern kern, dim3 grid, int threads, int smem, cudaStream_t st,
-                             const Args&... args) {
+cudaError_t launch_clustered(const char* name, Kern kern, dim3 grid, int cluster, int threads, int smem,
+                             cudaStream_t st, const Args&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     TraceScope trace(name, st);
     return keep(cudaLaunchKernelEx(&cfg, kern, args...));
+}
+
+template <typename Kern, typename... Args>
+cudaError_t launch_dependent(const char* name, Kern kern, dim3 grid, int threads, int smem, cudaStream_t st,
+                             const Args&... args) {
+    return launch_clustered(name, kern, grid, 1, threads, smem, st, args...);
 }
 
 dim3 flat_grid(int64_t items, int num_sms) {
@@ -305,15 +317,30 @@ int rank_grad(const GroupCtx& c, bool is_b, const uint16_t* act, const uint16_t*
 }
 
 // ------------------------------------------------------------------ fused products
-template <bool DX, int MSUB, bool DROP>
-cudaError_t launch_group_gemm(const char* name, const CUtensorMap* m, const GroupGemmArgs& g, dim3 grid,
-                              cudaStream_t st) {
-    using C = GroupGemmConfig<DX, MSUB>;
+// m: the maps of k_group_gemm, those of the tokens (0 and 2) still to be made.
+struct FusedMaps {
+    CUtensorMap m[4];
+    const uint16_t *act, *pair;
+    int64_t contraction, pair_cols, M;
+};
+
+template <bool DX, int T, bool DROP>
+cudaError_t launch_group_gemm(const char* name, FusedMaps& f, GroupGemmArgs g, int64_t col_tiles, bool cols_fastest,
+                              bool* mapped, cudaStream_t st) {
+    using C = GroupGemmConfig<DX, T>;
     static bool done[64] = {};
-    const cudaError_t e = opt_in(reinterpret_cast<const void*>(&k_group_gemm<DX, MSUB, DROP>), C::kSmem, done);
+    const cudaError_t e = opt_in(reinterpret_cast<const void*>(&k_group_gemm<DX, T, DROP>), C::kSmem, done);
     if (e != cudaSuccess) return keep(e);
-    return launch_dependent(name, k_group_gemm<DX, MSUB, DROP>, grid, C::kThreads, C::kSmem, st, m[0], m[1], m[2],
-                            m[3], g);
+    *mapped = map16(&f.m[0], f.act, f.contraction, f.M, 0, C::kSubT / 2) &&
+              map16(&f.m[2], f.pair, f.pair_cols, f.M, 0, C::kSubT / 2);
+    if (!*mapped) return cudaSuccess;
+    const int64_t row_tiles = most_tiles(g.offsets, g.E, g.M, T);
+    g.cols_fastest = cols_fastest && row_tiles <= 65535;
+    dim3 grid = g.cols_fastest ? dim3(static_cast<unsigned>(col_tiles), static_cast<unsigned>(row_tiles))
+                               : dim3(static_cast<unsigned>(row_tiles), static_cast<unsigned>(col_tiles));
+    grid.x *= 2;  // the two CTAs of a pair
+    return launch_clustered(name, k_group_gemm<DX, T, DROP>, grid, 2, C::kThreads, C::kSmem, st, f.m[0], f.m[1],
+                            f.m[2], f.m[3], g);
 }
 
 // Y (act X, pair T2, factor B) or dX (act dY, pair V2, factor A).
@@ -336,37 +363,41 @@ int fused(const GroupCtx& c, bool dx, const uint16_t* act, const uint16_t* pair,
     g.w_blocks_per_row = static_cast<int>(c.K / 64);
     g.out = out;
     g.drop = c.drop;
-    CUtensorMap m[4];
-    std::memset(m, 0, sizeof(m));
-    if (!map16(&m[0], act, contraction, c.M, 0, 128) || !map16(&m[2], pair, 2 * r64, c.M, 0, 128)) return -1;
-    if (dx ? !map_packed(&m[1], c.codes, c.N, c.K, c.E, 128, 64) || !map16(&m[3], factor, c.K, c.r, c.E, 64)
-           : !map_packed(&m[1], c.codes, c.N, c.K, c.E, 32, 256) ||
-                 !map16(&m[3], factor, ceil_to(c.r, 8), c.N, c.E, 256))
+    FusedMaps f;
+    std::memset(f.m, 0, sizeof(f.m));
+    f.act = act;
+    f.pair = pair;
+    f.contraction = contraction;
+    f.pair_cols = 2 * r64;
+    f.M = c.M;
+    if (dx ? !map_packed(&f.m[1], c.codes, c.N, c.K, c.E, 64, 64) || !map16(&f.m[3], factor, c.K, c.r, c.E, 64)
+           : !map_packed(&f.m[1], c.codes, c.N, c.K, c.E, 32, 128) ||
+                 !map16(&f.m[3], factor, ceil_to(c.r, 8), c.N, c.E, 128))
         return -1;
     const int64_t col_tiles = div_up(cols, 256);
-    // 256-row tiles halve the decode per MMA; they need enough tiles for every
-    // SM and groups of more than 128 rows
-    const bool wide = likely_tiles(c.E, c.M, 256) * col_tiles >= c.num_sms && c.M > 128 * int64_t(c.E);
-    const int64_t row_tiles = most_tiles(c.offsets, c.E, c.M, wide ? 256 : 128);
     // The tiles that run together share what they re-read.  Column tiles
-    // fastest reads the activations once and a group's weight once per row
+    // fastest reads the activations once and a group's weight once per token
     // tile of that group, from L2 where the weight fits it; one dense weight
-    // that does not goes row tiles fastest unless the activations are larger.
-    g.cols_fastest = (c.offsets != nullptr || 2 * c.M * contraction > c.N * c.K * 33 / 64) && row_tiles <= 65535;
-    const dim3 grid = g.cols_fastest ? dim3(static_cast<unsigned>(col_tiles), static_cast<unsigned>(row_tiles))
-                                     : dim3(static_cast<unsigned>(row_tiles), static_cast<unsigned>(col_tiles));
+    // that does not goes token tiles fastest unless the activations are larger.
+    const bool cols_fastest = c.offsets != nullptr || 2 * c.M * contraction > c.N * c.K * 33 / 64;
     const bool drop = dx && c.drop.threshold != 0;
-    cudaError_t e;
-    if (!dx)
-        e = wide ? launch_group_gemm<false, 2, false>("group_gemm_fwd", m, g, grid, c.stream)
-                 : launch_group_gemm<false, 1, false>("group_gemm_fwd", m, g, grid, c.stream);
-    else if (drop)
-        e = wide ? launch_group_gemm<true, 2, true>("group_gemm_dx_drop", m, g, grid, c.stream)
-                 : launch_group_gemm<true, 1, true>("group_gemm_dx_drop", m, g, grid, c.stream);
-    else
-        e = wide ? launch_group_gemm<true, 2, false>("group_gemm_dx", m, g, grid, c.stream)
-                 : launch_group_gemm<true, 1, false>("group_gemm_dx", m, g, grid, c.stream);
-    return e == cudaSuccess ? 0 : -2;
+    // tokens per tile, by the mean group
+    const int64_t mean = c.M / std::min<int64_t>(c.E, c.M);
+    bool mapped = false;
+    auto go = [&](auto t) {
+        constexpr int T = decltype(t)::value;
+        return !dx    ? launch_group_gemm<false, T, false>("group_gemm_fwd", f, g, col_tiles, cols_fastest, &mapped,
+                                                           c.stream)
+               : drop ? launch_group_gemm<true, T, true>("group_gemm_dx_drop", f, g, col_tiles, cols_fastest, &mapped,
+                                                         c.stream)
+                      : launch_group_gemm<true, T, false>("group_gemm_dx", f, g, col_tiles, cols_fastest, &mapped,
+                                                          c.stream);
+    };
+    const cudaError_t e = mean > 96   ? go(std::integral_constant<int, 512>())
+                          : mean > 32 ? go(std::integral_constant<int, 128>())
+                                      : go(std::integral_constant<int, 64>());
+    if (e != cudaSuccess) return -2;
+    return mapped ? 0 : -1;
 }
 
 // B as the tensor maps can read it: itself, or its padded copy.
