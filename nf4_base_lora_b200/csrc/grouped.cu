@@ -162,9 +162,51 @@ int grad_splits(int E, int64_t M, int64_t out_rows, int num_sms) {
     return split_steps(div_up(out_rows, 256) * groups, div_up(div_up(M, groups), 64), num_sms).splits;
 }
 
+// How the fused product is cut: by a model of its time in clocks, from the
+// measured parts (per step of a tile 2 clocks a token of MMAs, at least the
+// decode's share; per tile its start, its end and the stores of its results; for
+// a split contraction the partials' way through memory and one more kernel).
+// The groups are taken as equal, which the host has to.
+struct FusedPlan {
+    bool few;       // 32-token tiles, two CTAs per SM, steps of 128; else up to 512 tokens, one, of 64
+    int tile_rows;
+    int splits;
+    int k_main, k_ext;  // steps
+};
+
+FusedPlan plan_fused(int E, int64_t M, int64_t cols, int64_t contraction, int r, int num_sms) {
+    const int64_t groups = std::min<int64_t>(E, M), mean = div_up(M, groups), col_tiles = div_up(cols, 256);
+    FusedPlan best{};
+    best.few = mean <= 24;
+    const int wide = best.few ? 128 : 64;
+    best.k_main = static_cast<int>(div_up(contraction, wide));
+    best.k_ext = 2 * rank64(r) / wide;
+    double best_cost = 1e30;
+    const int64_t pairs = num_sms / 2 * (best.few ? 2 : 1);
+    for (int rows = best.few ? 32 : 512; rows >= 32; rows -= 32) {
+        const int64_t per_group = div_up(mean, rows), size = ceil_to(div_up(mean, per_group), 32);
+        const int64_t tiles = groups * per_group * col_tiles;
+        // many tokens: only to put work on every SM at all
+        const int most = best.few ? 8 : static_cast<int>(std::min<int64_t>(8, pairs / tiles));
+        for (int splits = 1; splits <= std::max(1, most) && (splits == 1 || splits * 4 <= best.k_main); ++splits) {
+            const double rounds = static_cast<double>(div_up(tiles * splits, pairs));
+            const double step = best.few ? 1400.0 : std::max(2.1 * size + 250.0, 500.0);
+            double cost = rounds * (step * static_cast<double>(div_up(best.k_main, splits) + best.k_ext) + 3000.0 +
+                                    16.0 * size);
+            if (splits > 1) cost += 6000.0 + static_cast<double>(splits) * M * cols * 8 / 2000.0;
+            if (cost < 0.97 * best_cost) {
+                best_cost = cost;
+                best.tile_rows = rows;
+                best.splits = splits;
+            }
+        }
+    }
+    return best;
+}
+
 struct Workspace {
     uint16_t *T2, *V2, *B8;
-    float* part;
+    float *part, *fused_part;
     int64_t bytes;
 };
 
@@ -188,6 +230,11 @@ Workspace layout(uint8_t* base, int64_t M, int E, int64_t N, int64_t K, int r, i
         if (sa > 1) part = std::max(part, sa * E * K * rn);
     }
     w.part = reinterpret_cast<float*>(take(part * 4));
+    // apart from the rank-r partials, whose sum may still run when the fused
+    // product's first tiles end
+    const int64_t cols = backward ? K : N;
+    const FusedPlan f = plan_fused(E, M, cols, backward ? N : K, r, num_sms);
+    if (f.splits > 1) w.fused_part = reinterpret_cast<float*>(take(f.splits * M * cols * 4));
     w.bytes = off;
     return w;
 }
@@ -325,7 +372,7 @@ struct FusedMaps {
 };
 
 template <bool DX, int T, bool DROP>
-cudaError_t launch_group_gemm(const char* name, FusedMaps& f, GroupGemmArgs g, int64_t col_tiles, bool cols_fastest,
+cudaError_t launch_group_gemm(const char* name, FusedMaps& f, GroupGemmArgs g, bool cols_fastest, int num_sms,
                               bool* mapped, cudaStream_t st) {
     using C = GroupGemmConfig<DX, T>;
     static bool done[64] = {};
@@ -334,27 +381,32 @@ cudaError_t launch_group_gemm(const char* name, FusedMaps& f, GroupGemmArgs g, i
     *mapped = map16(&f.m[0], f.act, f.contraction, f.M, 0, C::kSubT / 2) &&
               map16(&f.m[2], f.pair, f.pair_cols, f.M, 0, C::kSubT / 2);
     if (!*mapped) return cudaSuccess;
-    const int64_t row_tiles = most_tiles(g.offsets, g.E, g.M, T);
-    g.cols_fastest = cols_fastest && row_tiles <= 65535;
-    dim3 grid = g.cols_fastest ? dim3(static_cast<unsigned>(col_tiles), static_cast<unsigned>(row_tiles))
-                               : dim3(static_cast<unsigned>(row_tiles), static_cast<unsigned>(col_tiles));
-    grid.x *= 2;  // the two CTAs of a pair
+    const int64_t row_tiles = most_tiles(g.offsets, g.E, g.M, g.tile_rows);
+    g.row_tiles = cols_fastest ? -1 : static_cast<int>(row_tiles);
+    // one CTA (or two) on every SM, each pair walking its share of the tiles
+    const int64_t pairs =
+        std::min<int64_t>(num_sms / 2 * C::kMinBlocks, row_tiles * g.col_tiles * g.splits);
+    const dim3 grid(static_cast<unsigned>(2 * pairs));
     return launch_clustered(name, k_group_gemm<DX, T, DROP>, grid, 2, C::kThreads, C::kSmem, st, f.m[0], f.m[1],
                             f.m[2], f.m[3], g);
 }
 
 // Y (act X, pair T2, factor B) or dX (act dY, pair V2, factor A).
-int fused(const GroupCtx& c, bool dx, const uint16_t* act, const uint16_t* pair, const uint16_t* factor,
+int fused(const GroupCtx& c, bool dx, const uint16_t* act, const uint16_t* pair, const uint16_t* factor, float* part,
           uint16_t* out) {
     const int64_t contraction = dx ? c.N : c.K, cols = dx ? c.K : c.N;
     const int r64 = rank64(c.r);
+    const FusedPlan plan = plan_fused(c.E, c.M, cols, contraction, c.r, c.num_sms);
     GroupGemmArgs g{};
     g.offsets = c.offsets;
     g.E = c.E;
     g.M = static_cast<int>(c.M);
     g.cols = static_cast<int>(cols);
-    g.k_main = static_cast<int>(div_up(contraction, 64));
-    g.k_ext = 2 * r64 / 64;
+    g.k_main = plan.k_main;
+    g.k_ext = plan.k_ext;
+    g.splits = plan.splits;
+    g.tile_rows = plan.tile_rows;
+    g.col_tiles = static_cast<int>(div_up(cols, 256));
     g.qscale = c.qscale;
     g.scale2 = c.scale2;
     g.scale_mean = c.scale_mean;
@@ -362,6 +414,7 @@ int fused(const GroupCtx& c, bool dx, const uint16_t* act, const uint16_t* pair,
     g.w_rows = static_cast<int>(c.N);
     g.w_blocks_per_row = static_cast<int>(c.K / 64);
     g.out = out;
+    g.part = part;
     g.drop = c.drop;
     FusedMaps f;
     std::memset(f.m, 0, sizeof(f.m));
@@ -374,30 +427,32 @@ int fused(const GroupCtx& c, bool dx, const uint16_t* act, const uint16_t* pair,
            : !map_packed(&f.m[1], c.codes, c.N, c.K, c.E, 32, 128) ||
                  !map16(&f.m[3], factor, ceil_to(c.r, 8), c.N, c.E, 128))
         return -1;
-    const int64_t col_tiles = div_up(cols, 256);
     // The tiles that run together share what they re-read.  Column tiles
     // fastest reads the activations once and a group's weight once per token
     // tile of that group, from L2 where the weight fits it; one dense weight
     // that does not goes token tiles fastest unless the activations are larger.
     const bool cols_fastest = c.offsets != nullptr || 2 * c.M * contraction > c.N * c.K * 33 / 64;
     const bool drop = dx && c.drop.threshold != 0;
-    // tokens per tile, by the mean group
-    const int64_t mean = c.M / std::min<int64_t>(c.E, c.M);
     bool mapped = false;
     auto go = [&](auto t) {
         constexpr int T = decltype(t)::value;
-        return !dx    ? launch_group_gemm<false, T, false>("group_gemm_fwd", f, g, col_tiles, cols_fastest, &mapped,
+        return !dx    ? launch_group_gemm<false, T, false>("group_gemm_fwd", f, g, cols_fastest, c.num_sms, &mapped,
                                                            c.stream)
-               : drop ? launch_group_gemm<true, T, true>("group_gemm_dx_drop", f, g, col_tiles, cols_fastest, &mapped,
+               : drop ? launch_group_gemm<true, T, true>("group_gemm_dx_drop", f, g, cols_fastest, c.num_sms, &mapped,
                                                          c.stream)
-                      : launch_group_gemm<true, T, false>("group_gemm_dx", f, g, col_tiles, cols_fastest, &mapped,
+                      : launch_group_gemm<true, T, false>("group_gemm_dx", f, g, cols_fastest, c.num_sms, &mapped,
                                                           c.stream);
     };
-    const cudaError_t e = mean > 96   ? go(std::integral_constant<int, 512>())
-                          : mean > 32 ? go(std::integral_constant<int, 128>())
-                                      : go(std::integral_constant<int, 64>());
+    cudaError_t e = plan.few ? go(std::integral_constant<int, 32>()) : go(std::integral_constant<int, 512>());
     if (e != cudaSuccess) return -2;
-    return mapped ? 0 : -1;
+    if (!mapped) return -1;
+    if (plan.splits > 1) {
+        e = launch_dependent("group_sum", k_group_sum, flat_grid(c.M * cols / 4, c.num_sms), 256, 0, c.stream,
+                             c.offsets, c.E, static_cast<int>(c.M), static_cast<int>(cols), plan.splits,
+                             static_cast<const float*>(part), out);
+        if (e != cudaSuccess) return -2;
+    }
+    return 0;
 }
 
 // B as the tensor maps can read it: itself, or its padded copy.
@@ -432,7 +487,7 @@ int group_fwd(const GroupCtx& c, const uint16_t* A, const uint16_t* B, const uin
     const Workspace w = layout(ws, c.M, c.E, c.N, c.K, c.r, c.num_sms, false);
     int rc = padded_b(c, B, w.B8);
     if (rc == 0) rc = rank_rows(c, true, X, A, w.T2, T_saved, w.part);
-    if (rc == 0) rc = fused(c, false, X, w.T2, B, Y);
+    if (rc == 0) rc = fused(c, false, X, w.T2, B, w.fused_part, Y);
     return rc;
 }
 
@@ -444,7 +499,7 @@ int group_bwd(const GroupCtx& c, const uint16_t* A, const uint16_t* B, const uin
         rc = padded_b(c, B, w.B8);
         if (rc == 0) rc = rank_rows(c, false, dY, B, w.V2, nullptr, w.part);
     }
-    if (rc == 0 && dX != nullptr) rc = fused(c, true, dY, w.V2, A, dX);
+    if (rc == 0 && dX != nullptr) rc = fused(c, true, dY, w.V2, A, w.fused_part, dX);
     if (rc == 0 && dB != nullptr) {
         if (T_saved == nullptr) {
             rc = rank_rows(c, true, X, A, w.T2, nullptr, w.part);

@@ -14,21 +14,30 @@
 // steps of 32: a ragged tail costs little and one kernel serves groups of one
 // token and of thousands.
 //
-// The groups' bounds are device data, so the grid covers the most token tiles
-// any split of M rows into E groups can need; each warp finds its tile by a scan
-// of the offsets, and a pair beyond the last tile leaves.  A tile never crosses
-// a group: rows of the next group that its copies bring in are accumulator
-// columns that are not stored, or beyond N altogether.
+// The pairs are persistent: pair i takes the tiles i, i + pairs, ... and keeps
+// its barriers, rings and tensor memory; the copies of the next tile run while
+// the epilogue of the last one empties the accumulators.  The groups' bounds are
+// device data: each warp finds a tile by a scan of the offsets, and the first
+// tile beyond the last group ends the walk.  A group of n rows is divided evenly
+// into tiles of at most tile_rows.  A tile never crosses a group: rows of the
+// next group that its copies bring in are accumulator columns that are not
+// stored, or beyond N altogether.  With few tokens the contraction is split too
+// (fp32 partials, added in order by k_group_sum), so that the tiles divide evenly
+// over the pairs.
 //
 // Weights and factors are three-dimensional tensor maps (inner, row, expert):
 // rows beyond an expert's own read as zeros and never as the next expert's, so
 // a NaN or an infinity in one expert's adapter cannot reach another's result.
 //
-// Warp roles, in each CTA: warp 0 copies (TMA, one lane); warp 1 owns tensor
-// memory, and in the leading CTA its first lane issues the MMAs; teams of four
-// warps decode k-steps in turn (one (weight row, block) unit per thread, register
-// codebook) and then run the epilogue.  The rank-r term enters the same
-// accumulator as extension k-steps over [hi | lo] of the 16-bit pair of T or V.
+// Warp roles, in each CTA: warp 0 copies (TMA); warp 1 owns tensor memory and in
+// the leading CTA issues the MMAs; teams of four warps decode k-steps in turn
+// (one (weight row, block) unit per thread, register codebook) and run the
+// epilogue.  Three rings: tokens, packed codes (a few steps further ahead, so
+// that a decode never waits behind the tokens) and decoded tiles.  One barrier of
+// the leading CTA collects, for a step, the bytes of both CTAs' tokens and both
+// teams' arrivals: the issuing thread waits once a step.  The rank-r term enters
+// the same accumulator as extension k-steps over [hi | lo] of the 16-bit pair of
+// T or V.
 //
 // Dropout (input gradient): the extension steps come first, the epilogue warps
 // read the accumulators back, keep and scale them in fp32 and store them to
@@ -78,7 +87,7 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
 struct GroupTile {
     int e;        // expert
     int row0;     // first row of the tile
-    int row_end;  // end of the group's rows
+    int row_end;  // end of its rows (EVEN tiles) or of the group's
 };
 
 // Bounds of group e, clamped into 0 <= begin <= end <= M, so that offsets that
@@ -88,60 +97,115 @@ __device__ __forceinline__ void group_bounds(const int32_t* offsets, int e, int 
     end = min(max(__ldcg(offsets + e + 1), begin), M);
 }
 
-// Tile t of all groups' tiles of `tile_rows` rows, in group order; the whole
-// warp calls it.  False beyond the last tile.
-__device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int M, int tile_rows, int t, int lane,
+// Tile t of all groups' tiles of at most `most` rows, in group order; the whole
+// warp calls it.  EVEN: a group's tiles are of one size, a multiple of 32, else
+// all but its last have `most` rows.  False beyond the last tile.
+template <bool EVEN>
+__device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int M, int most, int t, int lane,
                                           GroupTile& g) {
-    if (offsets == nullptr) {
-        g.e = 0;
-        g.row0 = t * tile_rows;
-        g.row_end = M;
-        return g.row0 < M;
-    }
-    int before = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-        const int e = e0 + lane;
-        int begin = 0, end = 0;
-        if (e < E) group_bounds(offsets, e, M, begin, end);
-        const int n = (end - begin + tile_rows - 1) / tile_rows;
-        int incl = n;
+    int begin = 0, end = M, first = 0;
+    g.e = 0;
+    if (offsets != nullptr) {
+        bool found = false;
+        for (int e0 = 0; e0 < E && !found; e0 += 32) {
+            const int e = e0 + lane;
+            begin = end = 0;
+            if (e < E) group_bounds(offsets, e, M, begin, end);
+            const int n = (end - begin + most - 1) / most;
+            int incl = n;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-            if (lane >= d) incl += v;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+                if (lane >= d) incl += v;
+            }
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, first + incl > t);
+            if (hit != 0) {
+                const int src = __ffs(hit) - 1;
+                g.e = e0 + src;
+                first += __shfl_sync(0xFFFFFFFFu, incl - n, src);
+                begin = __shfl_sync(0xFFFFFFFFu, begin, src);
+                end = __shfl_sync(0xFFFFFFFFu, end, src);
+                found = true;
+            } else {
+                first += __shfl_sync(0xFFFFFFFFu, incl, 31);
+            }
         }
-        const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + incl > t);
-        if (hit != 0) {
-            const int src = __ffs(hit) - 1;
-            g.e = e0 + src;
-            const int excl = __shfl_sync(0xFFFFFFFFu, incl - n, src);
-            g.row0 = __shfl_sync(0xFFFFFFFFu, begin, src) + (t - before - excl) * tile_rows;
-            g.row_end = __shfl_sync(0xFFFFFFFFu, end, src);
-            return true;
-        }
-        before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        if (!found) return false;
     }
-    return false;
+    int size = most;
+    if (EVEN) {
+        const int n = end - begin, k = (n + most - 1) / most;
+        size = k > 0 ? ((n + k - 1) / k + 31) & ~31 : most;
+    }
+    g.row0 = begin + (t - first) * size;
+    g.row_end = EVEN ? min(end, g.row0 + size) : end;
+    return g.row0 < end;
 }
 
-// ------------------------------------------------------------------ CTA pairs
-__device__ __forceinline__ void mma2_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// ------------------------------------------------------------------ one thread of a warp
+// The MMA and copy instructions take their operands from uniform registers.
+// They are issued from code that the whole (converged) warp runs on uniform
+// values, by the one thread that elect.sync names; under a condition on the lane
+// index the compiler has to assume that values differ between threads and wraps
+// every such instruction in a loop over them (measured: about 120 clocks an MMA).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
+}
+
+__device__ __forceinline__ void mma1_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
-// Arrive once on `bar` of both CTAs of the pair when every MMA issued so far by
-// this thread has completed.
-__device__ __forceinline__ void mma2_commit(uint64_t* bar) {
+// Arrive once on `bar` when every MMA issued so far has completed.
+__device__ __forceinline__ void mma1_commit_elect(uint64_t* bar) {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
+// ------------------------------------------------------------------ CTA pairs
+__device__ __forceinline__ void mma2_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive once on `bar` of both CTAs of the pair when every MMA issued so far
+// has completed.
+__device__ __forceinline__ void mma2_commit_elect(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
             smem_u32(bar)),
         "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+// A copy into this CTA's shared memory that completes on a barrier of either CTA
+// of the pair (a shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* map, uint32_t cluster_bar,
+                                                 int32_t x, int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y)
         : "memory");
 }
 
@@ -165,15 +229,52 @@ __device__ __forceinline__ void tmem2_dealloc(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// ------------------------------------------------------------------ decode
+// One (weight row, 64-block) unit: 32 packed bytes to 64 bf16, written as the 8
+// swizzled 16-byte chunks of one 128-byte row (dst: the row's address with the
+// swizzle's XOR already in it).  The look-up is that of csrc/decode.cuh with the
+// selectors formed for a whole code word; the byte permutes and logic run on the
+// integer pipe at half rate and are what the decode is bound by, so the shifts
+// are written as high halves of products, which run on the multiply pipe.
+__device__ __forceinline__ void decode_row(const uint8_t* src, float s, uint8_t* dst) {
+    uint32_t P[4], H[4];
+    nf4_table(s, P, H);
+    const uint4 c0 = *reinterpret_cast<const uint4*>(src);
+    const uint4 c1 = *reinterpret_cast<const uint4*>(src + 16);
+    const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+    const uint32_t at = smem_u32(dst);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t w = words[j];
+        const uint32_t sel = w & 0x77777777u;                                     // index within 0-7 / 8-15
+        const uint32_t pick = (__umulhi(w, 0x80000000u) & 0x44444444u) | 0x32103210u;  // from 8-15 if bit 3
+        uint32_t o[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t se = h ? __umulhi(sel, 0x10000u) : sel, pk = h ? __umulhi(pick, 0x10000u) : pick;
+            const uint32_t lo = __byte_perm(__byte_perm(P[0], P[1], se), __byte_perm(P[2], P[3], se), pk);
+            const uint32_t hi = __byte_perm(__byte_perm(H[0], H[1], se), __byte_perm(H[2], H[3], se), pk);
+            o[2 * h] = __byte_perm(lo, hi, 0x4051);
+            o[2 * h + 1] = __byte_perm(lo, hi, 0x6273);
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (j << 4)), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                     "r"(o[3])
+                     : "memory");
+    }
+}
+
 // ------------------------------------------------------------------ fused product
 struct GroupGemmArgs {
     const int32_t* offsets;  // [E + 1], or NULL
     int E;
     int M;
     int cols;                // forward: N; input gradient: K
-    int k_main;              // 64-wide steps of the contraction
-    int k_ext;               // extension steps: 2 r64 / 64
-    int cols_fastest;        // 1: the pairs along grid.x walk the column tiles, else the row tiles
+    int k_main;              // steps of the contraction (64 kKS wide)
+    int k_ext;               // extension steps over 2 r64 (split 0)
+    int splits;              // parts of the contraction; > 1: partials
+    int tile_rows;           // at most, a multiple of 32
+    int col_tiles;
+    int row_tiles;           // walked first when >= 0 (one dense group, its exact count), else the column tiles are
     // encoded weight: rows and blocks of one expert
     const int8_t* qscale;
     const float* scale2;
@@ -182,35 +283,39 @@ struct GroupGemmArgs {
     int w_rows;
     int w_blocks_per_row;
     uint16_t* out;           // [M, cols]
+    float* part;             // [splits][M][cols]
     DropArgs drop;           // input gradient with dropout only
 };
 
-// T tokens per tile.  512: one CTA per SM, four teams; 128 and 64: two CTAs per
-// SM of two teams each, whose starts and ends overlap.
+// T tokens per tile at most.  512: one CTA per SM, four teams, steps of 64; 32:
+// two CTAs per SM of two teams each, whose starts and ends overlap, and steps of
+// 128 (kKS = 2 units per thread), which halve the barrier waits per decoded
+// weight where the decode is what takes the time.
 template <bool DX, int T>
 struct GroupGemmConfig {
     static constexpr int kBM = 128;                    // weight columns of one CTA
     static constexpr int kSubs = T > 256 ? 2 : 1;      // accumulators
     static constexpr int kSubT = T / kSubs;            // tokens of one, half of them per CTA
-    static constexpr int kTeams = T > 128 ? 4 : 2;
-    static constexpr int kDS = T == 128 ? 2 : 4;       // decoded tiles of 16 KB
-    static constexpr int kLS = 4;                      // load slots: codes and tokens
+    static constexpr int kTeams = T > 64 ? 4 : 2;
+    static constexpr int kKS = T > 64 ? 1 : 2;         // 64s of the contraction in a step
+    static constexpr int kDS = T > 64 ? 4 : 2;         // slots of decoded tiles and of tokens
+    static constexpr int kLC = 2 * kDS;                // slots of packed codes
     static constexpr int kSub = kSubT / 2 * 128;       // a CTA's tokens of one accumulator, 64 deep
-    static constexpr int kTokBytes = kSubs * kSub;
-    static constexpr int kCBytes = kBM * 32;           // packed codes of a step
-    static constexpr int kWBytes = kBM * 128;          // decoded tile
-    static constexpr int kLoadSlot = kTokBytes + kCBytes;
-    static constexpr int kSmem = kLS * kLoadSlot + kDS * kWBytes + 1024;
+    static constexpr int kTok = kSubs * kSub;          // of all accumulators
+    static constexpr int kCodes = kBM * 32, kW = kBM * 128;  // a packed and a decoded tile, 64 deep
+    static constexpr int kTokBytes = kKS * kTok, kCBytes = kKS * kCodes, kWBytes = kKS * kW;
+    static constexpr int kSmem = kDS * (kTokBytes + kWBytes) + kLC * kCBytes + 1024;
     static constexpr int kTeamThreads = kBM;           // one (row, block) unit each
     static constexpr int kTeamWarps = kTeamThreads / 32;
     static constexpr int kWorkWarps = kTeamWarps * kTeams;
     static constexpr int kThreads = 64 + 32 * kWorkWarps;
-    static constexpr int kMinBlocks = T > 128 ? 1 : 2;
+    static constexpr int kMinBlocks = T > 64 ? 1 : 2;
     static constexpr int kTmemCols = T < 32 ? 32 : T;
     static constexpr uint32_t kIdesc = make_idesc_bf16(2 * kBM, 0, DX ? 1 : 0, 0);  // without N
-    static_assert(kLS <= 2 * kDS, "the copies' waits on a decode slot could not tell its phases apart");
-    static_assert(kLS % kTeams == 0 && kDS % kTeams == 0, "a ring slot is one team's");
-    static_assert(kLoadSlot % 1024 == 0 && kSmem * kMinBlocks <= 226 * 1024, "shared memory");
+    // a wait for a barrier's phase is sound only where the phase before it is
+    // known to be complete: a slot is always the same team's
+    static_assert(kDS % kTeams == 0 && kLC % kTeams == 0 && kLC >= kDS, "rings");
+    static_assert(kSub % 1024 == 0 && kSmem * kMinBlocks <= 226 * 1024, "shared memory");
 };
 
 // map_t: X [M, K] or dY [M, N], box {64, kSubT / 2}.  map_w: codes (K / 2, N,
@@ -224,14 +329,13 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                  const GroupGemmArgs args) {
     using C = GroupGemmConfig<DX, T>;
     static_assert(DX || !DROP, "only the input gradient masks its accumulator");
-    constexpr int LS = C::kLS, DS = C::kDS;
+    constexpr int LC = C::kLC, DS = C::kDS;
     constexpr int kWork = C::kWorkWarps * 32;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    // bar_ready and bar_masked count both CTAs' arrivals, in the leading CTA
-    // (rank 0); the rest are each CTA's own, and the MMAs' completions arrive in
-    // both
-    __shared__ uint64_t bar_full[LS], bar_empty[LS], bar_ready[DS], bar_dempty[DS], bar_accum, bar_ext,
-        bar_masked;
+    // bar_ready, bar_masked and bar_free count both CTAs, in the leading one
+    // (rank 0); the MMAs' completions (bar_done, bar_accum, bar_ext) arrive in
+    // both; bar_codes is each CTA's own
+    __shared__ uint64_t bar_codes[LC], bar_ready[DS], bar_done[DS], bar_accum, bar_ext, bar_masked, bar_free;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
 
@@ -241,50 +345,66 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
     // the offsets, the activations and the encoded weight were complete before
     // the kernel this one depends on released it (that kernel waited for all
     // earlier ones first); T2 / V2 is that kernel's and is waited for below
-    GroupTile g;
-    const int pair = blockIdx.x >> 1;
-    const int ct = args.cols_fastest ? pair : blockIdx.y;
-    const int rt = args.cols_fastest ? blockIdx.y : pair;
-    if (!find_tile(args.offsets, args.E, args.M, T, rt, lane, g)) {
-        // every CTA waits, so this grid's completion implies the earlier kernels'
-        grid_dependency_wait();
-        return;
-    }
+
+    // A tile of this pair.  Its steps: n_main of the contraction from kb0 on, and
+    // in the first split the n_ext extension steps -- after them, or with dropout
+    // before.
+    struct Tile {
+        GroupTile g;
+        int h0;      // weight columns of this CTA
+        int tokens;
+        int nsub;
+        int z, kb0, n_main, n_ext;
+    };
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    auto next_tile = [&](int tl, Tile& t) {
+        int i = pair + tl * pairs;
+        t.z = 0;
+        if (args.splits > 1) {
+            t.z = i % args.splits;
+            i /= args.splits;
+        }
+        const int ct = args.row_tiles >= 0 ? i / args.row_tiles : i % args.col_tiles;
+        const int rt = args.row_tiles >= 0 ? i % args.row_tiles : i / args.col_tiles;
+        if (ct >= args.col_tiles || !find_tile<true>(args.offsets, args.E, args.M, args.tile_rows, rt, lane, t.g))
+            return false;
+        t.h0 = (2 * ct + rank) * C::kBM;
+        t.tokens = t.g.row_end - t.g.row0;
+        t.nsub = C::kSubs == 2 && t.tokens > C::kSubT ? 2 : 1;
+        t.kb0 = static_cast<int>(static_cast<int64_t>(args.k_main) * t.z / args.splits);
+        t.n_main = static_cast<int>(static_cast<int64_t>(args.k_main) * (t.z + 1) / args.splits) - t.kb0;
+        t.n_ext = t.z == 0 ? args.k_ext : 0;
+        return true;
+    };
+    // N of accumulator s, and the first of the rows that this CTA brings for it
+    auto sub_n = [&](const Tile& t, int s) { return (min(C::kSubT, t.tokens - s * C::kSubT) + 31) & ~31; };
+    auto sub_row = [&](const Tile& t, int s) { return t.g.row0 + s * C::kSubT + rank * (sub_n(t, s) >> 1); };
+    auto main0 = [&](const Tile& t) { return DROP ? t.n_ext : 0; };
+    auto is_main = [&](const Tile& t, int it) { return DROP ? it >= t.n_ext : it < t.n_main; };
+
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-    auto t_buf = [&](int it) { return base + (it % LS) * C::kLoadSlot; };
-    auto codes_buf = [&](int it) { return base + (it % LS) * C::kLoadSlot + C::kTokBytes; };
-    auto w_buf = [&](int it) { return base + LS * C::kLoadSlot + (it % DS) * C::kWBytes; };
-    const int h0 = (2 * ct + rank) * C::kBM;  // weight columns of this CTA
-    const int tokens = min(T, g.row_end - g.row0);
-    const int nsub = C::kSubs == 2 && tokens > C::kSubT ? 2 : 1;
-    // N of accumulator s, and the first of the rows that this CTA brings for it
-    auto sub_n = [&](int s) { return (min(C::kSubT, tokens - s * C::kSubT) + 31) & ~31; };
-    auto sub_row = [&](int s) { return g.row0 + s * C::kSubT + rank * (sub_n(s) >> 1); };
-    const int n_main = args.k_main, n_ext = args.k_ext, n_iter = n_main + n_ext;
-    // iteration it: the extension steps come last, or first with dropout
-    auto is_main = [&](int it) { return DROP ? it >= n_ext : it < n_main; };
-    const int main0 = DROP ? n_ext : 0, ext0 = DROP ? 0 : n_main;
+    // buffers of running step gi (counted over the pair's tiles), code slot cs
+    auto t_buf = [&](int gi) { return base + (gi % DS) * C::kTokBytes; };
+    auto w_buf = [&](int gi) { return base + DS * C::kTokBytes + (gi % DS) * C::kWBytes; };
+    auto codes_buf = [&](int cs) { return base + DS * (C::kTokBytes + C::kWBytes) + cs * C::kCBytes; };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < LS; ++i) {
-            mbar_init(&bar_full[i], 1);
-            mbar_init(&bar_empty[i], 1);
-        }
+        for (int i = 0; i < LC; ++i) mbar_init(&bar_codes[i], 1);
         for (int i = 0; i < DS; ++i) {
-            mbar_init(&bar_ready[i], 2 * C::kTeamWarps);
-            mbar_init(&bar_dempty[i], 1);
+            mbar_init(&bar_ready[i], 1 + 2 * C::kTeamWarps);
+            mbar_init(&bar_done[i], 1);
         }
         mbar_init(&bar_accum, 1);
         mbar_init(&bar_ext, 1);
         mbar_init(&bar_masked, 2 * C::kWorkWarps);
+        mbar_init(&bar_free, 2 * C::kWorkWarps);
         s_abort = 0;
         fence_barrier_init();
     }
-    // both CTAs' barriers are initialised once the cluster barrier is passed;
-    // thread 0, the producer, touches only its own and goes straight on
+    // both CTAs' barriers are initialised once this barrier is passed
     cluster_arrive_release();
-    if (threadIdx.x != 0) cluster_wait_acquire();
+    cluster_wait_acquire();
     volatile int* abort_flag = &s_abort;
     // the leading CTA's copy of a barrier (shared::cluster address)
     auto lead = [&](uint64_t* bar) { return cluster_map(smem_u32(bar), 0); };
@@ -296,43 +416,98 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             tma_prefetch_desc(&map_w);
             tma_prefetch_desc(&map_te);
             tma_prefetch_desc(&map_we);
-            int issued = 0;
-            for (int it = 0; it < n_iter; ++it) {
-                if (it >= LS && !mbar_wait(&bar_empty[it % LS], ((it / LS) & 1u) ^ 1u, abort_flag)) break;
-                if (*abort_flag) break;
-                uint64_t* bar = &bar_full[it % LS];
-                if (is_main(it)) {
-                    const int kb = it - main0;
-                    mbar_arrive_expect_tx(bar, nsub * C::kSub + C::kCBytes);
-                    for (int ms = 0; ms < nsub; ++ms)
-                        tma_load_2d(t_buf(it) + ms * C::kSub, &map_t, bar, kb * 64, sub_row(ms));
-                    if constexpr (DX) tma_load_3d(codes_buf(it), &map_w, bar, h0 / 2, kb * 64, g.e);
-                    else tma_load_3d(codes_buf(it), &map_w, bar, kb * 32, h0, g.e);
-                } else {
-                    const int j = it - ext0;
-                    // the factor's tile lands in a decode slot
-                    if (it >= DS && !mbar_wait(&bar_dempty[it % DS], ((it / DS) & 1u) ^ 1u, abort_flag)) break;
-                    if (j == 0) grid_dependency_wait();
-                    const int jb = j % (n_ext / 2);  // [hi | lo] against the factor twice
-                    mbar_arrive_expect_tx(bar, nsub * C::kSub + C::kWBytes);
-                    for (int ms = 0; ms < nsub; ++ms)
-                        tma_load_2d(t_buf(it) + ms * C::kSub, &map_te, bar, j * 64, sub_row(ms));
-                    if constexpr (DX) {
+        }
+        __syncwarp();
+        int gi = 0;
+        bool waited = false;
+        // the codes run kAhead steps before the tokens, into the next tile
+        constexpr int kAhead = LC - DS;
+        Tile tc, tt;  // tiles of the codes' and of the tokens' step
+        int tlc = 0, itc = 0, cs = 0;
+        bool have_c = next_tile(0, tc);
+        // packed codes of step itc, or nothing on an extension step, whose factor
+        // tile goes with its tokens
+        auto codes_step = [&]() {
+            if (!have_c) return;
+            if (is_main(tc, itc) && elect_one()) {
+                uint64_t* bar = &bar_codes[cs];
+                mbar_arrive_expect_tx(bar, C::kCBytes);
+                const int kb = (tc.kb0 + itc - main0(tc)) * C::kKS;
 #pragma unroll
-                        for (int c = 0; c < C::kBM / 64; ++c)
-                            tma_load_3d(w_buf(it) + c * 8192, &map_we, bar, h0 + c * 64, jb * 64, g.e);
+                for (int h = 0; h < C::kKS; ++h) {
+                    uint8_t* dst = codes_buf(cs) + h * C::kCodes;
+                    if constexpr (DX) tma_load_3d(dst, &map_w, bar, tc.h0 / 2, (kb + h) * 64, tc.g.e);
+                    else tma_load_3d(dst, &map_w, bar, (kb + h) * 32, tc.h0, tc.g.e);
+                }
+            }
+            __syncwarp();
+            if (++cs == LC) cs = 0;
+            if (++itc == tc.n_main + tc.n_ext) {
+                itc = 0;
+                have_c = next_tile(++tlc, tc);
+            }
+        };
+        for (int i = 0; i < kAhead; ++i) codes_step();
+        int ws = 0;  // code slot of step gi
+        bool stop = false;
+        for (int tl = 0; !stop && next_tile(tl, tt); ++tl) {
+            const int n_iter = tt.n_main + tt.n_ext;
+            for (int it = 0; it < n_iter; ++it, ++gi) {
+                // step gi - DS is multiplied: its token and decode slots are free,
+                // and so is the code slot of step gi + kAhead, which its decode has
+                // read.  The warp stays together also when a wait gives up.
+                stop = __any_sync(0xFFFFFFFFu,
+                                  (gi >= DS && !mbar_wait(&bar_done[gi % DS], ((gi / DS) & 1u) ^ 1u, abort_flag)) ||
+                                      *abort_flag);
+                if (stop) break;
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(&bar_ready[gi % DS], 2 * C::kKS * tt.nsub * C::kSub);
+                    const uint32_t bar = lead(&bar_ready[gi % DS]);
+                    if (is_main(tt, it)) {
+                        const int kb = (tt.kb0 + it - main0(tt)) * C::kKS;
+#pragma unroll
+                        for (int h = 0; h < C::kKS; ++h)
+                            for (int ms = 0; ms < tt.nsub; ++ms)
+                                tma_load_2d_pair(t_buf(gi) + h * C::kTok + ms * C::kSub, &map_t, bar, (kb + h) * 64,
+                                                 sub_row(tt, ms));
                     } else {
-                        tma_load_3d(w_buf(it), &map_we, bar, jb * 64, h0, g.e);
+                        // [hi | lo] against the factor twice; the factor's tile
+                        // lands in the decode slot
+                        const int j0 = (DROP ? it : it - tt.n_main) * C::kKS, half = tt.n_ext * C::kKS / 2;
+                        if (!waited) grid_dependency_wait();
+                        waited = true;
+                        uint64_t* wbar = &bar_codes[ws];
+                        mbar_arrive_expect_tx(wbar, C::kWBytes);
+#pragma unroll
+                        for (int h = 0; h < C::kKS; ++h) {
+                            const int j = j0 + h, jb = j % half;
+                            for (int ms = 0; ms < tt.nsub; ++ms)
+                                tma_load_2d_pair(t_buf(gi) + h * C::kTok + ms * C::kSub, &map_te, bar, j * 64,
+                                                 sub_row(tt, ms));
+                            uint8_t* dst = w_buf(gi) + h * C::kW;
+                            if constexpr (DX) {
+#pragma unroll
+                                for (int c = 0; c < C::kBM / 64; ++c)
+                                    tma_load_3d(dst + c * 8192, &map_we, wbar, tt.h0 + c * 64, jb * 64, tt.g.e);
+                            } else {
+                                tma_load_3d(dst, &map_we, wbar, jb * 64, tt.h0, tt.g.e);
+                            }
+                        }
                     }
                 }
-                ++issued;
+                __syncwarp();
+                if (++ws == LC) ws = 0;
+                codes_step();
             }
-            if (*abort_flag) {
-                // let the copies already issued land before the CTA exits
-                for (int it = issued > LS ? issued - LS : 0; it < issued; ++it)
-                    mbar_drain(&bar_full[it % LS], (it / LS) & 1u);
-            }
-            cluster_wait_acquire();  // the first phase, which every other thread passed at the start
+        }
+        // a pair without extension steps waits too, so that this grid's
+        // completion implies that of the kernels before it
+        if (!waited) grid_dependency_wait();
+        if (stop) {
+            // let the copies already issued land before the CTA exits (those
+            // that complete in the other CTA: by time)
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 1000000) {}
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ tensor memory, MMAs
@@ -341,62 +516,90 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
         asm volatile("bar.arrive 2, %0;" ::"r"(32 + kWork) : "memory");
         __syncwarp();
         tc_fence_after();
-        const uint32_t tmem_d = s_tmem;
-        if (lane == 0 && rank == 0) {
-            uint32_t idesc[2];
-            for (int ms = 0; ms < 2; ++ms) idesc[ms] = C::kIdesc | (static_cast<uint32_t>(max(32, sub_n(ms)) >> 3) << 17);
-            for (int it = 0; it < n_iter; ++it) {
-                // both CTAs' operands are in place: the one wait of a step
-                if (!mbar_wait(&bar_ready[it % DS], (it / DS) & 1u, abort_flag)) break;
-                if (DROP && it == main0 && !mbar_wait(&bar_masked, 0, abort_flag)) break;
-                tc_fence_after();
-                const uint32_t w_base = smem_u32(w_buf(it)), t_base = smem_u32(t_buf(it));
+        if (rank == 0) {
+            // Everything here is uniform over the warp, and said to be (values that
+            // went through a shuffle from lane 0), so that descriptors stay in
+            // uniform registers and an MMA costs a few clocks to issue.
+            const uint32_t tmem_d = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
+            bool stop = false;
+            int gi = 0, n_masked = 0;
+            const uint64_t w_desc0 = tile_desc(smem_u32(w_buf(0)), DX, 0);
+            const uint64_t t_desc0 = tile_desc(smem_u32(t_buf(0)), false, 0);
+            constexpr uint32_t kWk = DX ? 2048 / 16 : 32 / 16, kTk = 32 / 16;  // next 16 of the contraction
+            for (int tl = 0; !stop; ++tl) {
+                Tile t;
+                if (!next_tile(tl, t)) break;
+                const int nsub = __shfl_sync(0xFFFFFFFFu, t.nsub, 0);
+                const int n_iter = __shfl_sync(0xFFFFFFFFu, t.n_main + t.n_ext, 0);
+                const int ext_last = DROP ? __shfl_sync(0xFFFFFFFFu, t.n_ext, 0) - 1 : -1;
+                const uint32_t idesc0 = __shfl_sync(
+                    0xFFFFFFFFu, C::kIdesc | (static_cast<uint32_t>(max(32, sub_n(t, 0)) >> 3) << 17), 0);
+                const uint32_t idesc1 = __shfl_sync(
+                    0xFFFFFFFFu, C::kIdesc | (static_cast<uint32_t>(max(32, sub_n(t, 1)) >> 3) << 17), 0);
+                // the last tile's accumulators have been read
+                if (tl > 0) stop = !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_free, (tl - 1) & 1u, abort_flag));
+                for (int it = 0; it < n_iter && !stop; ++it, ++gi) {
+                    // the tokens and the weight tiles of both CTAs are in place
+                    stop = !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_ready[gi % DS], (gi / DS) & 1u, abort_flag));
+                    if (stop) break;
+                    tc_fence_after();
+                    const uint64_t wd = w_desc0 + static_cast<uint32_t>(gi % DS) * (C::kWBytes / 16);
+                    const uint64_t td = t_desc0 + static_cast<uint32_t>(gi % DS) * (C::kTokBytes / 16);
+                    const uint32_t acc = it > 0 ? 1u : 0u;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const uint64_t wdesc = tile_desc(w_base, DX, kk);
-                    for (int ms = 0; ms < nsub; ++ms)
-                        mma2_bf16_ss(tmem_d + ms * C::kSubT, wdesc, tile_desc(t_base + ms * C::kSub, false, kk),
-                                     idesc[ms], it * 4 + kk > 0 ? 1u : 0u);
+                    for (int k = 0; k < 4 * C::kKS; ++k) {
+                        const uint64_t w16 = wd + (k / 4) * (C::kW / 16) + (k % 4) * kWk;
+                        const uint64_t t16 = td + (k / 4) * (C::kTok / 16) + (k % 4) * kTk;
+                        mma2_elect(tmem_d, w16, t16, idesc0, k > 0 ? 1u : acc);
+                        if (C::kSubs == 2 && nsub == 2)
+                            mma2_elect(tmem_d + C::kSubT, w16, t16 + C::kSub / 16, idesc1, k > 0 ? 1u : acc);
+                    }
+                    mma2_commit_elect(&bar_done[gi % DS]);
+                    if (DROP && it == ext_last) {
+                        mma2_commit_elect(&bar_ext);
+                        stop = !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_masked, n_masked++ & 1u, abort_flag));
+                    }
                 }
-                mma2_commit(&bar_empty[it % LS]);
-                mma2_commit(&bar_dempty[it % DS]);
-                if (DROP && it == n_ext - 1) mma2_commit(&bar_ext);
+                mma2_commit_elect(&bar_accum);
             }
-            mma2_commit(&bar_accum);
         }
-        __syncwarp();
     } else {
         const int ew = warp - 2;
         const int q = warp & 3;  // tensor memory lane quadrant of this warp
-        constexpr int kShare = C::kSubT / (C::kWorkWarps / 4);  // tokens of an accumulator per warp
-        static_assert(kShare % 32 == 0, "whole loads of 32 tokens");
+        const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+        // tokens of an accumulator per warp, whole loads of 32 (so that some warps
+        // have none where the tile is small)
+        constexpr int kParts = C::kWorkWarps / 4;
+        constexpr int kShare = C::kSubT / kParts < 32 ? 32 : C::kSubT / kParts;
+        static_assert(kShare % 32 == 0 && (kShare * kParts == C::kSubT || C::kSubT == 32), "shares");
         const int tbeg = (ew / 4) * kShare;
-        uint32_t tmem_d = 0;
-        // keep and scale V A, this warp's part of both accumulators
-        auto mask_accumulators = [&]() {
-            asm volatile("bar.sync 2, %0;" ::"r"(32 + kWork) : "memory");
-            tc_fence_after();
-            tmem_d = s_tmem;
-            KeepGen gen;
+        asm volatile("bar.sync 2, %0;" ::"r"(32 + kWork) : "memory");
+        tc_fence_after();
+        const uint32_t tmem_d = s_tmem;
+        // ------------------------------------------------------------ keep and scale V A
+        // this warp's part of the accumulators; n counts these calls
+        auto mask_accumulators = [&](const Tile& t, int n) {
             grid_dependency_wait();  // the generator's state may be as young as V
+            KeepGen gen;
             gen.init(args.drop);
-            if (mbar_wait(&bar_ext, 0, abort_flag)) {
+            if (__all_sync(0xFFFFFFFFu, mbar_wait(&bar_ext, n & 1u, abort_flag))) {
                 tc_fence_after();
-                const int col = h0 + q * 32 + lane;
-                for (int ms = 0; ms < nsub; ++ms) {
+                const int col = t.h0 + q * 32 + lane;
+                for (int ms = 0; ms < t.nsub; ++ms) {
 #pragma unroll 1
-                    for (int tt = tbeg; tt < tbeg + kShare && ms * C::kSubT + tt < tokens; tt += 32) {
-                        const uint32_t at = tmem_d + (static_cast<uint32_t>(q * 32) << 16) + ms * C::kSubT + tt;
+                    for (int tt = tbeg; tt < tbeg + kShare && ms * C::kSubT + tt < t.tokens; tt += 32) {
+                        const uint32_t at = tmem_d + lane_base + ms * C::kSubT + tt;
                         uint32_t v[32];
                         tmem_ld_32x32b_x32(at, v);
                         tmem_ld_wait();
-                        const int64_t row0 = g.row0 + ms * C::kSubT + tt;
+                        const int64_t row0 = t.g.row0 + ms * C::kSubT + tt;
 #pragma unroll
                         for (int o = 0; o < 4; ++o) {
                             // the eight lanes of a generator group draw it for eight
                             // tokens, one each, and exchange the decisions
                             uint32_t f[4];
-                            gen.flags(static_cast<uint64_t>((row0 + 8 * o + (lane & 7)) * args.cols + (col & ~7)) >> 3, f);
+                            gen.flags(static_cast<uint64_t>((row0 + 8 * o + (lane & 7)) * args.cols + (col & ~7)) >> 3,
+                                      f);
                             uint32_t bits = 0;
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
@@ -417,129 +620,194 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             __syncwarp();
             if (lane == 0) mbar_arrive_pair(lead(&bar_masked));
         };
+
         // ------------------------------------------------------------ decoders
-        {
-            const int team = ew / C::kTeamWarps;
-            const int dt = threadIdx.x - 64 - team * C::kTeamThreads;
-            const bool fp32_scales = args.absmax != nullptr;  // no double quantisation
-            const float mu = fp32_scales ? 0.0f : __ldg(args.scale_mean);
-            // This thread's unit of a step.  Forward: weight row h0 + dt, block
-            // kb.  Input gradient: weight row 64 kb + n_local, block cblk of this
-            // CTA's half, dealt so that the eight threads of a quarter warp store
-            // to distinct bank groups and read codes at most two to one.
-            constexpr int kCB = C::kBM / 64;
-            static_assert(kCB == 2, "unit mapping");
-            int n_local = dt, cblk = 0;
-            if constexpr (DX) {
-                const int qw = dt >> 3, i = dt & 7;
-                n_local = 8 * (qw >> 1) + i;
-                cblk = ((i >> 1) + qw) & 1;
-            }
-            const int dst_off = DX ? cblk * 8192 + n_local * 128 : dt * 128;
-            const int swz = DX ? n_local & 7 : dt & 7;
-            const int code_off = DX ? (n_local * kCB + cblk) * 32 : dt * 32;
-            const int64_t scale_row0 = static_cast<int64_t>(g.e) * args.w_rows;
-            // block scales are fetched kPf of this team's steps ahead
-            constexpr int kPf = 4;
-            int8_t q_pf[kPf];
-            float a2_pf[kPf];
-            bool ok_pf[kPf];
-            auto fetch = [&](int kb, int slot) {
-                const int wrow = DX ? kb * 64 + n_local : h0 + dt;
-                const int wblk = DX ? h0 / 64 + cblk : kb;
-                ok_pf[slot] = kb >= 0 && kb < n_main && wrow < args.w_rows && wblk < args.w_blocks_per_row;
-                if (ok_pf[slot]) {
-                    const int64_t b = (scale_row0 + wrow) * args.w_blocks_per_row + wblk;
+        const int team = ew / C::kTeamWarps;
+        const int dt = threadIdx.x - 64 - team * C::kTeamThreads;
+        const bool fp32_scales = args.absmax != nullptr;  // no double quantisation
+        const float mu = fp32_scales ? 0.0f : __ldg(args.scale_mean);
+        // This thread's unit of a step.  Forward: weight row h0 + dt, block kb.
+        // Input gradient: weight row 64 kb + n_local, block cblk of this CTA's
+        // columns, dealt so that the eight threads of a quarter warp store to
+        // distinct bank groups and read codes at most two to one.
+        constexpr int kCB = C::kBM / 64;
+        static_assert(kCB == 2, "unit mapping");
+        int n_local = dt, cblk = 0;
+        if constexpr (DX) {
+            const int qw = dt >> 3, i = dt & 7;
+            n_local = 8 * (qw >> 1) + i;
+            cblk = ((i >> 1) + qw) & 1;
+        }
+        const int dst_off = DX ? cblk * 8192 + n_local * 128 + ((n_local & 7) << 4) : dt * 128 + ((dt & 7) << 4);
+        const int code_off = DX ? (n_local * kCB + cblk) * 32 : dt * 32;
+        // The units' block scales are fetched one own step (several steps of the
+        // pair) ahead: an 8-bit code and the second-level scale, or the fp32 scale.
+        struct Scale {
+            uint32_t ok;  // bit h: the unit lies inside the expert's weight
+            int q[C::kKS];
+            float a2[C::kKS];
+        };
+        auto fetch = [&](const Tile& t, int it) {
+            Scale s;
+            s.ok = 0;
+            const int k = it - main0(t);
+            // the first unit's index among the weight's blocks, and the next one's
+            const int row0 = DX ? (t.kb0 + k) * C::kKS * 64 + n_local : t.h0 + dt;
+            const int blk0 = DX ? t.h0 / 64 + cblk : (t.kb0 + k) * C::kKS;
+            const int64_t b0 = (static_cast<int64_t>(t.g.e) * args.w_rows + row0) * args.w_blocks_per_row + blk0;
+#pragma unroll
+            for (int h = 0; h < C::kKS; ++h) {
+                s.q[h] = 0;
+                s.a2[h] = 0.0f;
+                const int64_t b = b0 + (DX ? static_cast<int64_t>(h) * 64 * args.w_blocks_per_row : h);
+                if (k >= 0 && k < t.n_main && row0 + (DX ? 64 * h : 0) < args.w_rows &&
+                    blk0 + (DX ? 0 : h) < args.w_blocks_per_row) {
+                    s.ok |= 1u << h;
                     if (fp32_scales) {
-                        q_pf[slot] = 0;
-                        a2_pf[slot] = __ldg(args.absmax + b);
+                        s.a2[h] = __ldg(args.absmax + b);
                     } else {
-                        q_pf[slot] = __ldg(args.qscale + b);
-                        a2_pf[slot] = __ldg(args.scale2 + (b >> 8));
+                        s.q[h] = __ldg(args.qscale + b);
+                        s.a2[h] = __ldg(args.scale2 + (b >> 8));
                     }
-                }
-            };
-#pragma unroll
-            for (int u = 0; u < kPf; ++u) fetch(team + u * C::kTeams - main0, u);
-            bool stop = false, masked = !DROP;
-            // a ring slot is always the same team's, so its waits see every phase
-            for (int it0 = team; it0 < n_iter && !stop; it0 += kPf * C::kTeams) {
-#pragma unroll
-                for (int u = 0; u < kPf; ++u) {
-                    const int it = it0 + u * C::kTeams;
-                    if (it >= n_iter) break;
-                    const bool valid = ok_pf[u];
-                    const float sc =
-                        valid ? (fp32_scales ? a2_pf[u] : nf4_block_scale(q_pf[u], a2_pf[u], mu)) : 0.0f;
-                    fetch(it - main0 + kPf * C::kTeams, u);
-                    if (DROP && !masked && it >= n_ext) {
-                        masked = true;
-                        mask_accumulators();
-                    }
-                    if (!mbar_wait(&bar_full[it % LS], (it / LS) & 1u, abort_flag)) {
-                        stop = true;
-                        break;
-                    }
-                    if (is_main(it)) {
-                        if (it >= DS && !mbar_wait(&bar_dempty[it % DS], ((it / DS) & 1u) ^ 1u, abort_flag)) {
-                            stop = true;
-                            break;
-                        }
-                        uint8_t* dst = w_buf(it) + dst_off;
-                        if (!valid) zero_row(dst);
-                        else decode_unit_reg(codes_buf(it) + code_off, sc, dst, swz);
-                    }
-                    // also on an extension step, whose operands the copies brought
-                    // whole: the arrival passes on that they have landed
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_pair(lead(&bar_ready[it % DS]));
                 }
             }
-            if (DROP && !masked) mask_accumulators();
-        }
-        // ------------------------------------------------------------ epilogue
-        if constexpr (!DROP) {
-            asm volatile("bar.sync 2, %0;" ::"r"(32 + kWork) : "memory");
+            return s;
+        };
+        // ------------------------------------------------------------ epilogue of tile tl
+        // Lane: weight column.  A pair of lanes swaps halves of two tokens' values,
+        // so that a store writes two tokens' 64-byte runs (fp32 partials: 128 bytes
+        // of one token).
+        auto epilogue = [&](const Tile& t, int tl) {
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_accum, tl & 1u, abort_flag) && !*abort_flag);
             tc_fence_after();
-            tmem_d = s_tmem;
-        }
-        const bool ok = mbar_wait(&bar_accum, 0, abort_flag);
-        tc_fence_after();
-        if (ok && !*abort_flag) {
-            // lane: weight column; a pair of lanes swaps halves of two tokens'
-            // values, so that a store writes two tokens' 64-byte runs
-            const int col = h0 + q * 32 + (lane & 30), odd = lane & 1;
-            for (int ms = 0; ms < nsub; ++ms) {
+            const uint32_t odd = lane & 1, sel = odd ? 0x3276u : 0x5410u;
+            const int col = t.h0 + q * 32 + lane, col2 = col & ~1;
+            for (int ms = 0; ok && ms < t.nsub; ++ms) {
 #pragma unroll 1
-                for (int tt = tbeg; tt < tbeg + kShare && ms * C::kSubT + tt < tokens; tt += 32) {
+                for (int tt = tbeg; tt < tbeg + kShare && ms * C::kSubT + tt < t.tokens; tt += 32) {
                     uint32_t v[32];
-                    tmem_ld_32x32b_x32(tmem_d + (static_cast<uint32_t>(q * 32) << 16) + ms * C::kSubT + tt, v);
+                    tmem_ld_32x32b_x32(tmem_d + lane_base + ms * C::kSubT + tt, v);
                     tmem_ld_wait();
-                    const int row = g.row0 + ms * C::kSubT + tt + odd;
-                    uint16_t* dst = args.out + static_cast<int64_t>(row) * args.cols + col;
+                    const int at = ms * C::kSubT + tt, left = t.tokens - at;
+                    if (args.splits > 1) {
+                        float* dst = args.part + (static_cast<int64_t>(t.z) * args.M + t.g.row0 + at) * args.cols + col;
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float give = __uint_as_float(odd ? v[j] : v[j + 1]);
-                        const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-                        const uint32_t two = odd ? pack_bf16x2(got, __uint_as_float(v[j + 1]))
-                                                 : pack_bf16x2(__uint_as_float(v[j]), got);
-                        // cols is a multiple of 8
-                        if (row + j < g.row_end && col < args.cols)
-                            *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(j) * args.cols) = two;
+                        for (int j = 0; j < 32; ++j)
+                            if (j < left && col < args.cols)
+                                dst[static_cast<int64_t>(j) * args.cols] = __uint_as_float(v[j]);
+                    } else {
+                        uint16_t* dst = args.out + static_cast<int64_t>(t.g.row0 + at + odd) * args.cols + col2;
+                        const int rows = col2 < args.cols ? left - static_cast<int>(odd) : 0;  // cols is a multiple of 8
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const uint32_t own = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                            const uint32_t two = __byte_perm(own, __shfl_xor_sync(0xFFFFFFFFu, own, 1), sel);
+                            if (j < rows) *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(j) * args.cols) = two;
+                        }
                     }
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(lead(&bar_free));
+            return ok;
+        };
+
+        Tile t;
+        bool have = next_tile(0, t), stop = false;
+        int gi = team, it = team;      // this team's next step, and its place in tile t
+        int cs = team, n_masked = 0;   // its code slot; parity of the slot's use in cp
+        uint32_t cp = 0;
+        Scale ahead{};
+        if (have) ahead = fetch(t, it);
+        for (int tl = 0; have && !stop; ++tl) {
+            const int n_iter = t.n_main + t.n_ext;
+            bool masked = !DROP || t.n_ext == 0;
+#pragma unroll 1
+            for (; it < n_iter; it += C::kTeams, gi += C::kTeams) {
+                const Scale now = ahead;
+                ahead = fetch(t, it + C::kTeams);
+                const bool main_step = is_main(t, it);
+                if (DROP && !masked && main_step) {
+                    masked = true;
+                    mask_accumulators(t, n_masked++);
+                }
+                float sc[C::kKS];
+#pragma unroll
+                for (int h = 0; h < C::kKS; ++h)
+                    sc[h] = !(now.ok >> h & 1u) ? 0.0f
+                            : fp32_scales       ? now.a2[h]
+                                                : nf4_block_scale(static_cast<int8_t>(now.q[h]), now.a2[h], mu);
+                const bool ok =
+                    mbar_wait(&bar_codes[cs], cp, abort_flag) &&
+                    (!main_step || gi < DS || mbar_wait(&bar_done[gi % DS], ((gi / DS) & 1u) ^ 1u, abort_flag));
+                stop = __any_sync(0xFFFFFFFFu, !ok);  // the warp stays together
+                if (stop) break;
+                if (main_step) {
+#pragma unroll
+                    for (int h = 0; h < C::kKS; ++h) {
+                        uint8_t* dst = w_buf(gi) + h * C::kW + dst_off;
+                        // outside the weight: a zero scale decodes to zeros
+                        decode_row(codes_buf(cs) + h * C::kCodes + code_off, sc[h], dst);
+                    }
+                }
+                // also on an extension step, whose factor tile the copies brought:
+                // the arrival passes on that it has landed
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(lead(&bar_ready[gi % DS]));
+                cs += C::kTeams;
+                if (cs >= LC) {
+                    cs -= LC;
+                    cp ^= 1u;
+                }
+            }
+            if (DROP && !masked) mask_accumulators(t, n_masked++);
+            const Tile done = t;
+            it -= n_iter;
+            have = !stop && next_tile(tl + 1, t);
+            if (have) ahead = fetch(t, it);
+            if (!epilogue(done, tl)) stop = true;
         }
     }
     // neither CTA frees its tensor memory or leaves while the other may still
     // use it, read its operands or arrive on its barriers
+    __syncwarp();
     tc_fence_before();
     cluster_arrive_release();
     cluster_wait_acquire();
     if (warp == 1) {
         tc_fence_after();
         tmem2_dealloc(s_tmem, C::kTmemCols);
+    }
+}
+
+// out [M, cols] = the splits' partials added in order; rows outside the groups
+// are left as they are.  cols is a multiple of 8.
+__global__ void k_group_sum(const int32_t* offsets, int E, int M, int cols, int splits, const float* __restrict__ part,
+                            uint16_t* __restrict__ out) {
+    grid_dependency_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int lo = 0, hi = M;
+    if (offsets != nullptr) {
+        lo = min(max(__ldcg(offsets), 0), M);
+        hi = min(max(__ldcg(offsets + E), lo), M);
+    }
+    const int quads = cols / 4;
+    const int64_t total = static_cast<int64_t>(hi - lo) * quads, slice = static_cast<int64_t>(M) * quads;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const float4* p = reinterpret_cast<const float4*>(part) + static_cast<int64_t>(lo) * quads + i;
+        float4 v = __ldcg(p);
+        for (int z = 1; z < splits; ++z) {
+            const float4 x = __ldcg(p + z * slice);
+            v.x += x.x;
+            v.y += x.y;
+            v.z += x.z;
+            v.w += x.w;
+        }
+        reinterpret_cast<uint2*>(out)[static_cast<int64_t>(lo) * quads + i] =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
 }
 

@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kRankThreads, 2)
     GroupTile g;
     int out0 = 0, begin = 0, n_steps, step0;
     if constexpr (!TOK) {
-        if (!find_tile(args.offsets, args.E, args.M, 128, blockIdx.x, lane, g)) return;
+        if (!find_tile<false>(args.offsets, args.E, args.M, 128, blockIdx.x, lane, g)) return;
         step0 = blockIdx.z * args.k_per_split;
         n_steps = min(args.k_per_split, args.k_steps - step0);
     } else {
