@@ -143,7 +143,7 @@ struct Split {
 // `steps` split into parts of at least four steps so that tiles x parts is
 // about `ctas`; no part is empty.
 Split split_steps(int64_t tiles, int64_t steps, int ctas) {
-    int64_t s = std::max<int64_t>(1, ctas / std::max<int64_t>(1, tiles));
+    int64_t s = std::max<int64_t>(1, (ctas + tiles / 2) / std::max<int64_t>(1, tiles));
     s = std::min(s, std::max<int64_t>(1, steps / 4));
     const int64_t per = div_up(steps, s);
     return {static_cast<int>(div_up(steps, per)), static_cast<int>(per)};
@@ -152,14 +152,24 @@ Split split_steps(int64_t tiles, int64_t steps, int ctas) {
 int rank_width(int r) { return static_cast<int>(ceil_to(r, 16)); }
 int rank64(int r) { return static_cast<int>(ceil_to(r, 64)); }
 
-// Contraction splits of T (steps over K) and V (over N), and the parts of a
-// group's rows of dB (out rows N) and dA (out rows K).
+// Contraction splits of T (steps over K) and V (over N): two CTAs per SM.
 Split rows_split(int E, int64_t M, int64_t contraction, int num_sms) {
-    return split_steps(likely_tiles(E, M, 128), div_up(contraction, 64), num_sms);
+    return split_steps(likely_tiles(E, M, 128), div_up(contraction, 64), 2 * num_sms);
 }
-int grad_splits(int E, int64_t M, int64_t out_rows, int num_sms) {
-    const int64_t groups = std::min<int64_t>(E, M);
-    return split_steps(div_up(out_rows, 256) * groups, div_up(div_up(M, groups), 64), num_sms).splits;
+
+// Steps of a part of a group's rows for dB (out rows N) and dA (out rows K): so
+// many that the parts of an even batch are about one per SM, at least eight.
+int grad_part_steps(int E, int64_t M, int64_t out_rows, int num_sms) {
+    const int64_t groups = std::min<int64_t>(E, M), steps = div_up(div_up(M, groups), 64);
+    const int64_t parts = std::max<int64_t>(1, num_sms / (div_up(out_rows, 256) * groups));
+    return static_cast<int>(std::max<int64_t>(8, div_up(steps, parts)));
+}
+// Parts of the longest group there can be, and partials in all: a group of n > p
+// steps has at most 2 n / p parts.
+int64_t most_parts(int64_t M, int part_steps) { return std::max<int64_t>(1, div_up(div_up(M, 64), part_steps)); }
+int64_t most_partials(int E, int64_t M, int part_steps) {
+    const int64_t one = most_parts(M, part_steps);
+    return one == 1 ? 0 : (E == 1 ? one : 2 * one);
 }
 
 // How the fused product is cut: by a model of its time in clocks, from the
@@ -225,9 +235,8 @@ Workspace layout(uint8_t* base, int64_t M, int E, int64_t N, int64_t K, int r, i
     int64_t part = rows_split(E, M, K, num_sms).splits * M * rn;
     if (backward) {
         part = std::max(part, rows_split(E, M, N, num_sms).splits * M * rn);
-        const int sb = grad_splits(E, M, N, num_sms), sa = grad_splits(E, M, K, num_sms);
-        if (sb > 1) part = std::max(part, sb * E * N * rn);
-        if (sa > 1) part = std::max(part, sa * E * K * rn);
+        part = std::max(part, most_partials(E, M, grad_part_steps(E, M, N, num_sms)) * N * rn);
+        part = std::max(part, most_partials(E, M, grad_part_steps(E, M, K, num_sms)) * K * rn);
     }
     w.part = reinterpret_cast<float*>(take(part * 4));
     // apart from the rank-r partials, whose sum may still run when the fused
@@ -258,15 +267,16 @@ __global__ void k_pad_columns(const uint16_t* __restrict__ src, int64_t rows, in
 template <int MODE, bool DROP>
 cudaError_t launch_rank(const char* name, const CUtensorMap& a, const CUtensorMap& b, RankArgs g, dim3 grid,
                         cudaStream_t st) {
-    constexpr bool tok = MODE == RANK_DB || MODE == RANK_DA;
+    using C = RankConfig<MODE, DROP>;
+    constexpr bool tok = C::kTok;
     const int rchunks = (g.rn + 63) / 64;
     g.a_bytes = tok ? 4 * 8192 : 16384;
     g.b_bytes = tok ? 2 * rchunks * 8192 : MODE == RANK_V ? rchunks * 8192 : g.rn * 128;
     const int slot = g.a_bytes + g.b_bytes;
-    // three stages or more of half an SM's shared memory, so that two CTAs
-    // overlap their ends; else what one CTA can have
-    int stages = std::min(kRankStages, 110 * 1024 / slot);
-    if (stages < 3) stages = std::min(kRankStages, 224 * 1024 / slot);
+    // half an SM's shared memory where that holds two stages, else what one CTA
+    // can have
+    int stages = std::min(kRankStages, 111 * 1024 / slot);
+    if (stages < 2) stages = std::min(kRankStages, 224 * 1024 / slot);
     g.stages = stages;
     const int cols = tok ? 2 * g.rn : g.rn;
     g.tmem_cols = 32;
@@ -274,7 +284,7 @@ cudaError_t launch_rank(const char* name, const CUtensorMap& a, const CUtensorMa
     static bool done[64] = {};
     const cudaError_t e = opt_in(reinterpret_cast<const void*>(&k_rank<MODE, DROP>), 226 * 1024, done);
     if (e != cudaSuccess) return keep(e);
-    return launch_dependent(name, k_rank<MODE, DROP>, grid, kRankThreads, stages * slot + 1024, st, a, b, g);
+    return launch_dependent(name, k_rank<MODE, DROP>, grid, C::kThreads, stages * slot + 1024, st, a, b, g);
 }
 
 RankArgs rank_args(const GroupCtx& c) {
@@ -334,33 +344,40 @@ int rank_rows(const GroupCtx& c, bool is_t, const uint16_t* act, const uint16_t*
 int rank_grad(const GroupCtx& c, bool is_b, const uint16_t* act, const uint16_t* pair, uint16_t* out, int accumulate,
               float* part) {
     const int64_t rows = is_b ? c.N : c.K;
-    const int splits = grad_splits(c.E, c.M, rows, c.num_sms);
+    const int part_steps = grad_part_steps(c.E, c.M, rows, c.num_sms);
+    const int64_t parts = most_parts(c.M, part_steps);
     const bool drop = !is_b && c.drop.threshold != 0;
     RankArgs g = rank_args(c);
     g.rows = static_cast<int>(rows);
-    g.splits = splits;
+    g.part_steps = part_steps;
+    g.slots = static_cast<int>(most_partials(c.E, c.M, part_steps));
     g.alpha = drop ? c.drop.gain : 1.0f;
     g.part = part;
-    g.part_slice = int64_t(c.E) * rows * g.rn;
-    g.out = splits == 1 ? out : nullptr;
+    g.part_slice = rows * g.rn;
+    g.out = out;
     g.accumulate = accumulate;
     CUtensorMap ma, mb;
     std::memset(&ma, 0, sizeof(ma));
     std::memset(&mb, 0, sizeof(mb));
     if (!map16(&ma, act, rows, c.M, 0, 64) || !map16(&mb, pair, 2 * g.r64, c.M, 0, 64)) return -1;
-    const dim3 grid(static_cast<unsigned>(div_up(rows, 256)), static_cast<unsigned>(c.E), splits);
+    const dim3 grid(static_cast<unsigned>(div_up(rows, 256)),
+                    static_cast<unsigned>(c.E == 1 ? parts : c.E + most_partials(c.E, c.M, part_steps)));
     const cudaError_t e = is_b   ? launch_rank<RANK_DB, false>("rank_db", ma, mb, g, grid, c.stream)
                           : drop ? launch_rank<RANK_DA, true>("rank_da_drop", ma, mb, g, grid, c.stream)
                                  : launch_rank<RANK_DA, false>("rank_da", ma, mb, g, grid, c.stream);
     if (e != cudaSuccess) return -2;
-    if (splits == 1) return 0;
-    const dim3 sum_grid = flat_grid(int64_t(c.E) * rows * c.r, c.num_sms);
+    if (parts == 1) return 0;
+    const bool vec = !is_b || c.r % 4 == 0;
+    dim3 sum_grid = flat_grid(rows * c.r / (vec ? 4 : 1), c.num_sms);
+    sum_grid.y = static_cast<unsigned>(c.E);
     auto sum = [&](auto kern) {
-        return launch_dependent("rank_grad_sum", kern, sum_grid, 256, 0, c.stream, static_cast<const float*>(part),
-                                splits, g.part_slice, static_cast<int64_t>(c.E), static_cast<int>(rows), c.r, g.rn,
-                                g.alpha, out, accumulate);
+        return launch_dependent("rank_grad_sum", kern, sum_grid, 256, 0, c.stream, c.offsets, c.E, g.M, part_steps,
+                                g.slots, static_cast<const float*>(part), static_cast<int>(rows), c.r, g.rn, g.alpha,
+                                out, accumulate);
     };
-    return (is_b ? sum(k_rank_grad_sum<false>) : sum(k_rank_grad_sum<true>)) == cudaSuccess ? 0 : -2;
+    return (!is_b ? sum(k_rank_grad_sum<true, 4>)
+            : vec ? sum(k_rank_grad_sum<false, 4>)
+                  : sum(k_rank_grad_sum<false, 1>)) == cudaSuccess ? 0 : -2;
 }
 
 // ------------------------------------------------------------------ fused products

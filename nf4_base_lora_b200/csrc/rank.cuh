@@ -9,21 +9,26 @@
 // All four read one large activation once and are bound by that stream (HBM);
 // the MMAs are N = r wide and idle most of the time.  T and V split the
 // contraction over grid.z into fp32 partials that k_rank_rows_sum adds in a
-// fixed order; dB and dA contract over a group's rows, 256 output rows per CTA
-// (two accumulators sharing the narrow operand), and write their result
-// themselves where the experts alone fill the SMs.  T and V enter dB and dA as
-// their 16-bit pair [hi | lo], both halves into the same accumulator columns.
+// fixed order.  dB and dA contract over a group's rows, 256 output rows per CTA
+// (two accumulators sharing the narrow operand); a long group is cut into parts
+// of at most part_steps steps, whose partials k_rank_grad_sum adds in order,
+// while a group of one part writes its result itself -- so a skewed batch does
+// not wait for its longest group, and short groups cost no partials.  T and V
+// enter dB and dA as their 16-bit pair [hi | lo], both halves into the same
+// accumulator columns.
 //
 // Dropout: the activation tile has landed in shared memory in the swizzled
 // operand layout, whose 16-byte pieces are exactly the generator's groups of
-// eight elements; eight warps clear the dropped elements of each piece in place
-// (the gain goes into the product's factor, so no kept element is rounded) and
-// hand the tile to the MMAs.  The last step of a group that does not end on a
+// eight elements; the clearing warps zero the dropped elements of each piece in
+// place (the gain goes into the product's factor, so no kept element is rounded)
+// and hand the tile to the MMAs.  The last step of a group that does not end on a
 // step's 64 rows gets the rows behind its end cleared the same way, in both
 // operands: they belong to the next group, or to nobody and may hold anything.
 //
 // Warp roles: warp 0 copies, warp 1 owns tensor memory and issues the MMAs,
-// warps 2 .. 9 clear elements and run the epilogue.
+// warps 2 .. 9 clear elements and run the epilogue.  Two CTAs share an SM wherever
+// two stages of each fit: their starts, which take as long as several steps, and
+// their ends overlap.
 #pragma once
 
 #include <cstdint>
@@ -43,7 +48,8 @@ struct RankArgs {
     int rows;          // dB: N, dA: K (output rows per expert)
     int k_steps;       // T, V: 64-wide steps of the contraction
     int k_per_split;   // T, V
-    int splits;        // dB, dA: parts of a group's rows
+    int part_steps;    // dB, dA
+    int slots;         // partials there is room for
     int r, rn;         // rank; MMA width, r rounded up to 16
     int r64;           // column of the low halves in T2 / V2
     int stages, a_bytes, b_bytes;
@@ -51,15 +57,80 @@ struct RankArgs {
     DropArgs drop;
     int drop_cols;     // K
     float alpha;       // dB, dA written here
-    float* part;       // T, V: [split][M][rn]; dB: [split][E][N][rn]; dA: [split][E][rn][K]
+    float* part;       // T, V: [split][M][rn]; dB: [part][N][rn]; dA: [part][rn][K]
     int64_t part_slice;
-    uint16_t* out;     // dB [E][N][r] / dA [E][r][K] written here, or NULL (partials)
+    uint16_t* out;     // dB [E][N][r] / dA [E][r][K]
     int accumulate;
 };
 
 constexpr int kRankStages = 8;  // at most
-constexpr int kRankWarps = 8;
-constexpr int kRankThreads = 64 + 32 * kRankWarps;
+template <int MODE, bool DROP>
+struct RankConfig {
+    static constexpr bool kTok = MODE == RANK_DB || MODE == RANK_DA;
+    static constexpr int kWarps = 8;  // clearing and epilogue
+    static constexpr int kThreads = 64 + 32 * kWarps;
+};
+
+// The parts of the groups' rows for dB and dA, numbered in group order: a group
+// has ceil(rows / (64 part_steps)) of them, at least one.
+struct RankPart {
+    int e;
+    int begin, end;  // the group's rows
+    int parts;       // of the group
+    int part;        // this one
+    int slot;        // of the group's first partial; groups of one part take none
+};
+// Part u (its group's first one where FIRST: u counts groups); the whole warp
+// calls it.  False beyond the last.  A group beyond the last slot, which only
+// offsets that break their rule can make, stays whole (its later parts are void).
+template <bool FIRST>
+__device__ __forceinline__ bool find_part(const int32_t* offsets, int E, int M, int part_steps, int slots, int u,
+                                          int lane, RankPart& p) {
+    auto count = [&](int n) { return max(1, (n + 64 * part_steps - 1) / (64 * part_steps)); };
+    p.slot = 0;
+    if (offsets == nullptr) {
+        p.e = 0;
+        p.begin = 0;
+        p.end = M;
+        p.parts = count(M);
+        p.part = FIRST ? 0 : u;
+        return p.part < p.parts && (!FIRST || u == 0);
+    }
+    int before = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + lane;
+        int begin = 0, end = 0, n = 0;
+        if (e < E) {
+            group_bounds(offsets, e, M, begin, end);
+            n = count(end - begin);
+        }
+        const int taken = n > 1 ? n : 0, units = FIRST ? (e < E ? 1 : 0) : n;
+        int incl = units, sl = taken;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d), w = __shfl_up_sync(0xFFFFFFFFu, sl, d);
+            if (lane >= d) {
+                incl += v;
+                sl += w;
+            }
+        }
+        const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + incl > u);
+        if (hit != 0) {
+            const int src = __ffs(hit) - 1;
+            p.e = e0 + src;
+            p.begin = __shfl_sync(0xFFFFFFFFu, begin, src);
+            p.end = __shfl_sync(0xFFFFFFFFu, end, src);
+            p.parts = __shfl_sync(0xFFFFFFFFu, n, src);
+            p.part = FIRST ? 0 : u - before - __shfl_sync(0xFFFFFFFFu, incl - units, src);
+            p.slot += __shfl_sync(0xFFFFFFFFu, sl - taken, src);
+            if (p.parts > 1 && p.slot + p.parts > slots) p.parts = 1;
+            return p.part < p.parts;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        p.slot += __shfl_sync(0xFFFFFFFFu, sl, 31);
+    }
+    return false;
+}
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) {
     const __nv_bfloat16 h = __float2bfloat16_rn(v);
@@ -70,13 +141,15 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
 // (MN-major).  map_b: T: A (K, r, E), box {64, rn, 1}; V: B (r, N, E), box
 // {64, 64, 1}; dB, dA: T2 / V2 [M, 2 r64], box {64, 64}.
 template <int MODE, bool DROP>
-__global__ void __launch_bounds__(kRankThreads, 2)
+__global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
     k_rank(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const RankArgs args) {
-    constexpr bool TOK = MODE == RANK_DB || MODE == RANK_DA;  // contraction over a group's rows
+    using C = RankConfig<MODE, DROP>;
+    constexpr bool TOK = C::kTok;  // contraction over a group's rows
     static_assert(!DROP || MODE == RANK_T || MODE == RANK_DA, "only X is dropped");
-    constexpr int kOutRows = TOK ? 256 : 128;
+    constexpr int kOutRows = TOK ? 256 : 128, kWork = 32 * C::kWarps;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ uint64_t bar_full[kRankStages], bar_empty[kRankStages], bar_clear[kRankStages], bar_last, bar_tail, bar_accum;
+    __shared__ uint64_t bar_full[kRankStages], bar_empty[kRankStages], bar_clear[kRankStages], bar_last, bar_tail,
+        bar_accum;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
 
@@ -87,47 +160,46 @@ __global__ void __launch_bounds__(kRankThreads, 2)
 
     GroupTile g;
     int out0 = 0, begin = 0, n_steps, step0;
+    RankPart part{0, 0, 0, 1, 0, 0};
     if constexpr (!TOK) {
         if (!find_tile<false>(args.offsets, args.E, args.M, 128, blockIdx.x, lane, g)) return;
         step0 = blockIdx.z * args.k_per_split;
         n_steps = min(args.k_per_split, args.k_steps - step0);
     } else {
-        g.e = blockIdx.y;
-        g.row_end = args.M;
-        if (args.offsets != nullptr) group_bounds(args.offsets, g.e, args.M, begin, g.row_end);
+        if (!find_part<false>(args.offsets, args.E, args.M, args.part_steps, args.slots, blockIdx.y, lane, part))
+            return;
+        g.e = part.e;
+        begin = part.begin;
+        g.row_end = part.end;
         out0 = blockIdx.x * kOutRows;
         const int total = (g.row_end - begin + 63) / 64;
-        const int per = (total + args.splits - 1) / args.splits;
-        step0 = blockIdx.z * per;
+        const int per = (total + part.parts - 1) / part.parts;
+        step0 = part.part * per;
         n_steps = max(0, min(per, total - step0));
     }
+    n_steps = __shfl_sync(0xFFFFFFFFu, n_steps, 0);  // said to be uniform, as what follows from it
     const int LS = args.stages, slot_bytes = args.a_bytes + args.b_bytes;
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-    auto a_buf = [&](int it) { return base + (it % LS) * slot_bytes; };
-    auto b_buf = [&](int it) { return base + (it % LS) * slot_bytes + args.a_bytes; };
     const int rchunks = (args.rn + 63) / 64;
     // rows of the group in the step after which it ends (64: no partial step here)
     int tail_rows = 64;
     if (TOK && n_steps > 0) tail_rows = min(64, g.row_end - (begin + 64 * (step0 + n_steps - 1)));
     // dense calls end where the array does, whose copies read zeros behind it
     const bool has_tail = TOK && args.offsets != nullptr && tail_rows < 64;
-
-    // The barrier on which step `it` lands, and its parity.  Without dropout the
-    // clearing warps look at the last step alone; a wait on the ring's barrier
-    // could not tell its phases apart there, so that step has a barrier of its own.
+    // The barrier on which step `it` lands.  Without dropout the clearing warps
+    // look at the last step alone; a wait on the ring's barrier could not tell its
+    // phases apart there, so that step has a barrier of its own.
     auto own_bar = [&](int it) { return !DROP && has_tail && it == n_steps - 1; };
-    auto full_bar = [&](int it) { return own_bar(it) ? &bar_last : &bar_full[it % LS]; };
-    auto full_parity = [&](int it) { return own_bar(it) ? 0u : (it / LS) & 1u; };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < LS; ++i) {
             mbar_init(&bar_full[i], 1);
             mbar_init(&bar_empty[i], 1);
-            mbar_init(&bar_clear[i], kRankWarps);
+            mbar_init(&bar_clear[i], C::kWarps);
         }
         mbar_init(&bar_last, 1);
-        mbar_init(&bar_tail, kRankWarps);
+        mbar_init(&bar_tail, C::kWarps);
         mbar_init(&bar_accum, 1);
         s_abort = 0;
         fence_barrier_init();
@@ -139,108 +211,143 @@ __global__ void __launch_bounds__(kRankThreads, 2)
         if (lane == 0) {
             tma_prefetch_desc(&map_a);
             tma_prefetch_desc(&map_b);
-            int issued = 0;
-            for (int it = 0; it < n_steps; ++it) {
-                if (it >= LS && !mbar_wait(&bar_empty[it % LS], ((it / LS) & 1u) ^ 1u, abort_flag)) break;
-                if (*abort_flag) break;
-                uint64_t* bar = full_bar(it);
+        }
+        __syncwarp();
+        int slot = 0;
+        uint32_t phase = 1;  // of the slot's release; passes at once in the first round
+        bool stop = false;
+        for (int it = 0; it < n_steps; ++it) {
+            stop = __any_sync(0xFFFFFFFFu, (it >= LS && !mbar_wait(&bar_empty[slot], phase, abort_flag)) || *abort_flag);
+            if (stop) break;
+            if (elect_one()) {
+                uint64_t* bar = own_bar(it) ? &bar_last : &bar_full[slot];
+                uint8_t* a_buf = base + slot * slot_bytes;
+                uint8_t* b_buf = a_buf + args.a_bytes;
                 const int k = 64 * (step0 + it);
                 mbar_arrive_expect_tx(bar, slot_bytes);
                 if constexpr (!TOK) {
-                    tma_load_2d(a_buf(it), &map_a, bar, k, g.row0);
+                    tma_load_2d(a_buf, &map_a, bar, k, g.row0);
                     if constexpr (MODE == RANK_T) {
-                        tma_load_3d(b_buf(it), &map_b, bar, k, 0, g.e);
+                        tma_load_3d(b_buf, &map_b, bar, k, 0, g.e);
                     } else {
-                        for (int c = 0; c < rchunks; ++c)
-                            tma_load_3d(b_buf(it) + c * 8192, &map_b, bar, 64 * c, k, g.e);
+                        for (int c = 0; c < rchunks; ++c) tma_load_3d(b_buf + c * 8192, &map_b, bar, 64 * c, k, g.e);
                     }
                 } else {
 #pragma unroll
                     for (int c = 0; c < kOutRows / 64; ++c)
-                        tma_load_2d(a_buf(it) + c * 8192, &map_a, bar, out0 + 64 * c, begin + k);
+                        tma_load_2d(a_buf + c * 8192, &map_a, bar, out0 + 64 * c, begin + k);
                     for (int c = 0; c < rchunks; ++c) {
-                        tma_load_2d(b_buf(it) + c * 8192, &map_b, bar, 64 * c, begin + k);
-                        tma_load_2d(b_buf(it) + (rchunks + c) * 8192, &map_b, bar, args.r64 + 64 * c, begin + k);
+                        tma_load_2d(b_buf + c * 8192, &map_b, bar, 64 * c, begin + k);
+                        tma_load_2d(b_buf + (rchunks + c) * 8192, &map_b, bar, args.r64 + 64 * c, begin + k);
                     }
                 }
-                ++issued;
             }
-            if (*abort_flag)
-                for (int it = issued > LS ? issued - LS : 0; it < issued; ++it)
-                    mbar_drain(full_bar(it), full_parity(it));
+            __syncwarp();
+            if (++slot == LS) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        }
+        if (stop) {
+            // let the copies already issued land before the CTA exits
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 1000000) {}
         }
     } else if (warp == 1) {
         tmem_alloc(&s_tmem, args.tmem_cols);
         tmem_relinquish();
         tc_fence_before();
-        asm volatile("bar.arrive 2, %0;" ::"r"(32 + 32 * kRankWarps) : "memory");
+        asm volatile("bar.arrive 2, %0;" ::"r"(32 + kWork) : "memory");
         __syncwarp();
         tc_fence_after();
-        const uint32_t tmem_d = s_tmem;
+        const uint32_t tmem_d = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
         const uint32_t idesc = make_idesc_bf16(128, 0, TOK ? 1 : 0, MODE == RANK_T ? 0 : 1) |
                                (static_cast<uint32_t>(args.rn >> 3) << 17);
-        if (lane == 0) {
-            for (int it = 0; it < n_steps; ++it) {
-                if (!mbar_wait(full_bar(it), full_parity(it), abort_flag)) break;
-                if (DROP) {
-                    if (!mbar_wait(&bar_clear[it % LS], (it / LS) & 1u, abort_flag)) break;
-                } else if (has_tail && it == n_steps - 1) {
-                    if (!mbar_wait(&bar_tail, 0, abort_flag)) break;
-                }
-                tc_fence_after();
-                const uint32_t a_base = smem_u32(a_buf(it)), b_base = smem_u32(b_buf(it));
+        constexpr uint32_t kAk = TOK ? 2048 / 16 : 32 / 16, kBk = MODE == RANK_T ? 32 / 16 : 2048 / 16;
+        const uint64_t a0 = tile_desc(smem_u32(base), TOK, 0);
+        const uint64_t b0 = tile_desc(smem_u32(base) + args.a_bytes, MODE != RANK_T, 0);
+        int slot = 0;
+        uint32_t phase = 0;
+        for (int it = 0; it < n_steps; ++it) {
+            const bool last = own_bar(it);
+            bool ok = mbar_wait(last ? &bar_last : &bar_full[slot], last ? 0u : phase, abort_flag);
+            if (DROP) ok = ok && mbar_wait(&bar_clear[slot], phase, abort_flag);
+            else if (last) ok = ok && mbar_wait(&bar_tail, 0, abort_flag);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            tc_fence_after();
+            const uint64_t at = a0 + static_cast<uint32_t>(slot) * (slot_bytes / 16);
+            const uint64_t bt = b0 + static_cast<uint32_t>(slot) * (slot_bytes / 16);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const uint32_t first = it * 4 + kk > 0 ? 1u : 0u;
-                    if constexpr (!TOK) {
-                        mma_bf16_ss(tmem_d, tile_desc(a_base, false, kk), tile_desc(b_base, MODE == RANK_V, kk), idesc,
-                                    first);
-                    } else {
-                        const uint64_t hi = tile_desc(b_base, true, kk);
-                        const uint64_t lo = tile_desc(b_base + rchunks * 8192, true, kk);
+            for (int kk = 0; kk < 4; ++kk) {
+                const uint32_t first = it * 4 + kk > 0 ? 1u : 0u;
+                if constexpr (!TOK) {
+                    mma1_elect(tmem_d, at + kk * kAk, bt + kk * kBk, idesc, first);
+                } else {
+                    const uint64_t hi = bt + kk * kBk, lo = hi + rchunks * (8192 / 16);
 #pragma unroll
-                        for (int ms = 0; ms < 2; ++ms) {
-                            const uint64_t a = tile_desc(a_base + ms * 16384, true, kk);
-                            mma_bf16_ss(tmem_d + ms * args.rn, a, hi, idesc, first);
-                            mma_bf16_ss(tmem_d + ms * args.rn, a, lo, idesc, 1u);
-                        }
+                    for (int ms = 0; ms < 2; ++ms) {
+                        mma1_elect(tmem_d + ms * args.rn, at + ms * (16384 / 16) + kk * kAk, hi, idesc, first);
+                        mma1_elect(tmem_d + ms * args.rn, at + ms * (16384 / 16) + kk * kAk, lo, idesc, 1u);
                     }
                 }
-                mma_commit(&bar_empty[it % LS]);
             }
-            mma_commit(&bar_accum);
+            mma1_commit_elect(&bar_empty[slot]);
+            if (++slot == LS) {
+                slot = 0;
+                phase ^= 1u;
+            }
         }
+        mma1_commit_elect(&bar_accum);
     } else {
         const int ew = warp - 2, wt = threadIdx.x - 64;
         // ------------------------------------------------------------ clearing
         if (DROP || has_tail) {
             KeepGen gen;
             if constexpr (DROP) gen.init(args.drop);
-            for (int it = DROP ? 0 : n_steps - 1; it < n_steps; ++it) {
-                if (!mbar_wait(full_bar(it), full_parity(it), abort_flag)) break;
-                uint8_t* a = a_buf(it);
+            const int it0 = DROP ? 0 : n_steps - 1;
+            int slot = it0 % LS;
+            uint32_t phase = (it0 / LS) & 1;
+            for (int it = it0; it < n_steps; ++it) {
+                const bool last = own_bar(it);
+                if (!__all_sync(0xFFFFFFFFu,
+                                mbar_wait(last ? &bar_last : &bar_full[slot], last ? 0u : phase, abort_flag)))
+                    break;
+                uint8_t* a = base + slot * slot_bytes;
                 const int k = 64 * (step0 + it);
                 if constexpr (DROP) {
-                    constexpr int kPieces = kOutRows * 8 / (32 * kRankWarps);  // 16-byte pieces per thread
+                    constexpr int kPieces = kOutRows * 8 / kWork;  // 16-byte pieces per thread
+                    // flat index in X, in groups of eight elements, of this thread's
+                    // first piece; the pieces of a thread are rows of one chunk
+                    // column, drop_cols / 8 groups per row apart
+                    const int c = wt & 7, row = wt >> 3;
+                    constexpr int kRowStep = kWork / 8;  // rows between a thread's pieces
+                    int64_t grp;
+                    if constexpr (!TOK)
+                        grp = (static_cast<int64_t>(g.row0 + row) * args.drop_cols + k + 8 * c) >> 3;
+                    else
+                        grp = (static_cast<int64_t>(begin + k + row % 64) * args.drop_cols + out0 + 64 * (row / 64) +
+                               8 * c) >> 3;
+                    const int gcols = args.drop_cols >> 3;
 #pragma unroll
                     for (int i = 0; i < kPieces; ++i) {
-                        const int p = wt + i * 32 * kRankWarps;
-                        const int c = p & 7;
                         int off;
-                        int64_t elem;  // flat index in X of the piece's first element
+                        uint64_t gi;
                         if constexpr (!TOK) {
-                            const int row = p >> 3;
-                            off = row * 128 + ((c ^ (row & 7)) << 4);
-                            elem = static_cast<int64_t>(g.row0 + row) * args.drop_cols + k + 8 * c;
+                            const int r = row + i * kRowStep;
+                            off = r * 128 + ((c ^ (r & 7)) << 4);
+                            gi = static_cast<uint64_t>(grp + static_cast<int64_t>(i * kRowStep) * gcols);
                         } else {
-                            const int chunk = p >> 9, row = (p >> 3) & 63;
-                            off = chunk * 8192 + row * 128 + ((c ^ (row & 7)) << 4);
-                            elem = static_cast<int64_t>(begin + k + row) * args.drop_cols + out0 + 64 * chunk + 8 * c;
+                            // rows run over the chunks: chunk r / 64, row r % 64 of it
+                            static_assert(kRowStep == 64 || kRowStep == 32 || !TOK, "rows of a chunk");
+                            const int r = row + i * kRowStep, chunk = r / 64, rr = r % 64;
+                            off = chunk * 8192 + rr * 128 + ((c ^ (rr & 7)) << 4);
+                            gi = static_cast<uint64_t>(grp + 8 * (chunk - row / 64) +
+                                                       static_cast<int64_t>(rr - row % 64) * gcols);
                         }
                         uint4* at = reinterpret_cast<uint4*>(a + off);
                         uint4 v = *at;
                         uint32_t m[4];
-                        gen.masks(static_cast<uint64_t>(elem) >> 3, m);
+                        gen.masks(gi, m);
                         v.x &= m[0];
                         v.y &= m[1];
                         v.z &= m[2];
@@ -250,28 +357,32 @@ __global__ void __launch_bounds__(kRankThreads, 2)
                 }
                 if (TOK && has_tail && it == n_steps - 1) {
                     // rows behind the group's end: whole 128-byte rows of every chunk
-                    if (DROP) named_barrier_sync(4, 32 * kRankWarps);  // the pieces above are other threads'
+                    if (DROP) named_barrier_sync(4, kWork);  // the pieces above are other threads'
+                    uint8_t* b_buf = a + args.a_bytes;
                     const int chunks = kOutRows / 64 + 2 * rchunks, per = (64 - tail_rows) * 8;
-                    for (int p = wt; p < chunks * per; p += 32 * kRankWarps) {
+                    for (int p = wt; p < chunks * per; p += kWork) {
                         const int chunk = p / per, rem = p - chunk * per;
-                        uint8_t* src = chunk < kOutRows / 64 ? a + chunk * 8192
-                                                             : b_buf(it) + (chunk - kOutRows / 64) * 8192;
+                        uint8_t* src = chunk < kOutRows / 64 ? a + chunk * 8192 : b_buf + (chunk - kOutRows / 64) * 8192;
                         *reinterpret_cast<uint4*>(src + tail_rows * 128 + rem * 16) = make_uint4(0, 0, 0, 0);
                     }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(DROP ? &bar_clear[it % LS] : &bar_tail);
+                if (lane == 0) mbar_arrive(DROP ? &bar_clear[slot] : &bar_tail);
+                if (++slot == LS) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
             }
         }
         // ------------------------------------------------------------ epilogue
-        asm volatile("bar.sync 2, %0;" ::"r"(32 + 32 * kRankWarps) : "memory");
+        asm volatile("bar.sync 2, %0;" ::"r"(32 + kWork) : "memory");
         tc_fence_after();
         const uint32_t tmem_d = s_tmem;
-        const int q = warp & 3, half = ew >> 2;
-        const bool ok = mbar_wait(&bar_accum, 0, abort_flag) && !*abort_flag;
+        const int q = warp & 3, half = (ew >> 2) & 1;
+        const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_accum, 0, abort_flag) && !*abort_flag);
         tc_fence_after();
-        if (ok && (n_steps > 0 || TOK)) {
+        if (ok && ew < 8) {
             // T, V: the two halves of the warps share the columns; dB, dA: they
             // take one accumulator each
             const int cols = TOK ? args.rn : args.rn / 2;
@@ -280,6 +391,7 @@ __global__ void __launch_bounds__(kRankThreads, 2)
             const int row = TOK ? out0 + lrow : g.row0 + lrow;
             const bool row_ok = row < (TOK ? args.rows : g.row_end);
             const uint32_t at = tmem_d + (static_cast<uint32_t>(q * 32) << 16) + (TOK ? half * args.rn : 0);
+            const bool direct = part.parts == 1;
             for (int cc = cbeg; cc < cbeg + cols; cc += 8) {
                 uint32_t v[8];
                 if (n_steps > 0) {
@@ -295,25 +407,32 @@ __global__ void __launch_bounds__(kRankThreads, 2)
                     *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
                     *reinterpret_cast<uint4*>(dst + 4) = make_uint4(v[4], v[5], v[6], v[7]);
                 } else if constexpr (MODE == RANK_DB) {
-                    if (args.out == nullptr) {
-                        float* dst = args.part + blockIdx.z * args.part_slice +
-                                     (static_cast<int64_t>(g.e) * args.rows + row) * args.rn + cc;
+                    if (!direct) {
+                        float* dst = args.part + static_cast<int64_t>(part.slot + part.part) * args.part_slice +
+                                     static_cast<int64_t>(row) * args.rn + cc;
                         *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
                         *reinterpret_cast<uint4*>(dst + 4) = make_uint4(v[4], v[5], v[6], v[7]);
                     } else {
                         uint16_t* dst = args.out + (static_cast<int64_t>(g.e) * args.rows + row) * args.r + cc;
+                        uint16_t o[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (cc + j < args.r) {
-                                float x = __uint_as_float(v[j]) * args.alpha;
-                                if (args.accumulate) x += bf16_bits_to_float(dst[j]);
-                                dst[j] = bf16_bits(x);
-                            }
+                        for (int j = 0; j < 8; ++j) {
+                            float x = __uint_as_float(v[j]) * args.alpha;
+                            if (args.accumulate && cc + j < args.r) x += bf16_bits_to_float(dst[j]);
+                            o[j] = bf16_bits(x);
+                        }
+                        if (args.r % 8 == 0) {
+                            if (cc < args.r) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (cc + j < args.r) dst[j] = o[j];
+                        }
                     }
                 } else {
-                    if (args.out == nullptr) {
-                        float* dst = args.part + blockIdx.z * args.part_slice +
-                                     (static_cast<int64_t>(g.e) * args.rn + cc) * args.rows + row;
+                    if (!direct) {
+                        float* dst = args.part + static_cast<int64_t>(part.slot + part.part) * args.part_slice +
+                                     static_cast<int64_t>(cc) * args.rows + row;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) dst[static_cast<int64_t>(j) * args.rows] = __uint_as_float(v[j]);
                     } else {
@@ -331,6 +450,7 @@ __global__ void __launch_bounds__(kRankThreads, 2)
             }
         }
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -419,30 +539,49 @@ __global__ void k_rank_pair(const float* __restrict__ src, int64_t M, int r, int
     }
 }
 
-// dB [E][N][r] (TRANSPOSED false) or dA [E][r][K] from partials
-// [split][E][N][rn] or [split][E][rn][K], the splits added in order.
-template <bool TRANSPOSED>
-__global__ void k_rank_grad_sum(const float* __restrict__ part, int splits, int64_t slice, int64_t E, int rows, int r,
-                                int rn, float alpha, uint16_t* __restrict__ out, int accumulate) {
+// dB [E][N][r] (TRANSPOSED false) or dA [E][r][K] of the groups of several parts,
+// from partials [part][N][rn] or [part][rn][K], added in order.  grid.y: expert.
+// VEC elements at a time (4 needs r to be a multiple of 4 where not TRANSPOSED).
+template <bool TRANSPOSED, int VEC>
+__global__ void __launch_bounds__(256)
+    k_rank_grad_sum(const int32_t* offsets, int E, int M, int part_steps, int slots, const float* __restrict__ part,
+                    int rows, int r, int rn, float alpha, uint16_t* __restrict__ out, int accumulate) {
     grid_dependency_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t total = E * rows * r;
+    RankPart p;
+    if (!find_part<true>(offsets, E, M, part_steps, slots, blockIdx.y, threadIdx.x & 31, p) || p.parts == 1) return;
+    const int64_t slice = static_cast<int64_t>(rows) * rn;
+    const int inner = (TRANSPOSED ? rows : r) / VEC, ld = TRANSPOSED ? rows : rn;
+    const int64_t total = static_cast<int64_t>(rows) * r / VEC;
+    const float* src = part + p.slot * slice;
+    uint16_t* dst = out + static_cast<int64_t>(p.e) * rows * r;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t inner = TRANSPOSED ? rows : r;
-        const int64_t outer = i / inner, c = i - outer * inner;
-        int64_t at;
-        if (TRANSPOSED) {
-            const int64_t e = outer / r, j = outer - e * r;
-            at = (e * rn + j) * rows + c;
-        } else {
-            at = outer * rn + c;
+        const int64_t outer = total < (int64_t(1) << 31) ? static_cast<int>(i) / inner : i / inner;
+        const float* at = src + outer * ld + (i - outer * inner) * VEC;
+        float v[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] = 0.0f;
+        for (int z = 0; z < p.parts; ++z, at += slice) {
+            if constexpr (VEC == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(at));
+                v[0] += x.x;
+                v[1] += x.y;
+                v[2] += x.z;
+                v[3] += x.w;
+            } else {
+                v[0] += __ldcg(at);
+            }
         }
-        float v = 0.0f;
-        for (int z = 0; z < splits; ++z) v += __ldcg(part + z * slice + at);
-        v *= alpha;
-        if (accumulate) v += bf16_bits_to_float(out[i]);
-        out[i] = bf16_bits(v);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            v[j] *= alpha;
+            if (accumulate) v[j] += bf16_bits_to_float(dst[i * VEC + j]);
+        }
+        if constexpr (VEC == 4)
+            reinterpret_cast<uint2*>(dst)[i] = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        else
+            dst[i] = bf16_bits(v[0]);
     }
 }
 
