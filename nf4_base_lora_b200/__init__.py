@@ -322,21 +322,56 @@ def qlora_linear_bwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, scaling: fl
 
 
 # ---------------------------------------------------------------- adapter dropout, experts
-def _matrix(t: Optional[torch.Tensor], name: str, dtype, shape, device) -> Optional[torch.Tensor]:
-    """`t` checked to be a contiguous CUDA tensor of this type, shape and device."""
-    if t is not None and (t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape)
-                          or t.device != device):
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
-                         % (name, str(dtype).replace("torch.", ""), list(shape), device))
-    return t
+# These calls are made once per layer and token in serving, so their own time on
+# the host is kept to a few microseconds: the stream as the raw handle (the
+# public accessor builds a stream object), a device switch only where it is
+# needed, messages only where a check fails.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_BF16, _F32 = torch.bfloat16, torch.float32
+
+
+def _refuse(t, name: str, dtype, shape, device) -> None:
+    raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
+                     % (name, str(dtype).replace("torch.", ""), list(shape), device))
+
+
+def _addr(t: Optional[torch.Tensor], name: str, dtype, shape, device) -> Optional[int]:
+    """The address of `t`, checked to be a contiguous tensor of this type and
+    shape on this (CUDA) device; None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, device)
+    return t.data_ptr()
 
 
 def _dropout(p: float, rng: Optional[torch.Tensor], device) -> LoraDropoutStruct:
     """The generator's state is a CUDA int64 tensor (seed, offset), read when
     the kernels run."""
-    if rng is not None:
-        _matrix(rng, "rng", torch.int64, (2,), device)
-    return LoraDropoutStruct(float(p), None if rng is None else rng.data_ptr())
+    return LoraDropoutStruct(p, _addr(rng, "rng", torch.int64, (2,), device))
+
+
+def _launch(fn, device, *args) -> None:
+    """fn(*args, stream) on the device's current stream."""
+    i = device.index
+    if torch.cuda.current_device() == i:
+        status = fn(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            status = fn(*args, _raw_stream(i))
+    if status != NF4_OK:
+        _check(status)
+
+
+def _ws_args(ws: Optional[torch.Tensor], need, sizes, device):
+    """(address, bytes) of the workspace, allocated where it is not given."""
+    if ws is None:
+        ws = _workspace(need(*sizes), device)
+        if ws is None:
+            return None, 0, None
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 def lora_dropout(X: torch.Tensor, p: float, rng: Optional[torch.Tensor],
@@ -346,14 +381,13 @@ def lora_dropout(X: torch.Tensor, p: float, rng: Optional[torch.Tensor],
     offset), a CUDA int64 tensor, and the element's index (lora_dropout_params
     in include/nf4lora.h).  The gradient is the same call on the incoming
     gradient.  `out` may be X."""
-    if X.dtype not in (torch.bfloat16, torch.float32) or not X.is_cuda or not X.is_contiguous():
+    dt, dev = X.dtype, X.device
+    if (dt is not _BF16 and dt is not _F32) or dev.type != "cuda" or not X.is_contiguous():
         raise ValueError("X must be a contiguous bfloat16 or float32 CUDA tensor")
-    _matrix(out, "out", X.dtype, X.shape, X.device)
-    with torch.cuda.device(X.device):
-        d = _dropout(p, rng, X.device)
-        out = out if out is not None else torch.empty_like(X)
-        _check(lib.lora_dropout(_ptr(X), X.numel(), 0 if X.dtype == torch.bfloat16 else 1, ctypes.byref(d), _ptr(out),
-                                _stream()))
+    if out is None:
+        out = torch.empty_like(X)
+    o = _addr(out, "out", dt, X.shape, dev)
+    _launch(lib.lora_dropout, dev, X.data_ptr(), X.numel(), 0 if dt is _BF16 else 1, _dropout(p, rng, dev), o)
     return out
 
 
@@ -373,61 +407,47 @@ def qlora_grouped_bwd_workspace_bytes(M: int, n_experts: int, d_out: int, d_in: 
     return int(lib.qlora_grouped_bwd_workspace_bytes(M, n_experts, d_out, d_in, r))
 
 
-def _group_shapes(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, lead: Tuple[int, ...]) -> Tuple[int, int]:
-    """(d_out of one expert, r) of an adapter whose tensors have the leading
-    dimensions `lead`; everything on the weight's device."""
-    dev = w.buffer.device
-    d_out = w.d_out // (lead[0] if lead else 1)
+def _group_fwd(fn, need, w, A, B, lead, scaling, X, offsets, p, rng, save_t, Y, workspace, T):
+    """Both forwards; lead: (n_experts,) and the offsets' address, or () and ()."""
+    dev, d_in = w.buffer.device, w.d_in
+    d_out = w.d_out // lead[0] if lead else w.d_out
     r = A.shape[-2] if A.dim() == 2 + len(lead) else 0
-    _matrix(A, "A", torch.bfloat16, lead + (r, w.d_in), dev)
-    _matrix(B, "B", torch.bfloat16, lead + (d_out, r), dev)
-    return d_out, r
-
-
-def _group_fwd(call, w, A, B, lead, X, p, rng, save_t, Y, workspace, T, need):
-    dev = w.buffer.device
-    d_out, r = _group_shapes(w, A, B, lead)
-    M = X.shape[0]
-    _matrix(X, "X", torch.bfloat16, (M, w.d_in), dev)
-    _matrix(Y, "Y", torch.bfloat16, (M, d_out), dev)
-    _matrix(T, "T", torch.float32, (M, r), dev)
-    with torch.cuda.device(dev):
-        Y = Y if Y is not None else torch.empty((M, d_out), dtype=torch.bfloat16, device=dev)
-        if not save_t:
-            T = None
-        elif T is None:
-            T = torch.empty((M, r), dtype=torch.float32, device=dev)
-        d = _dropout(p, rng, dev)
-        ws = workspace if workspace is not None else _workspace(need(M, *lead, d_out, w.d_in, r), dev)
-        _check(call(r, ctypes.byref(d), M, Y, T, ws))
+    M = X.shape[0] if X.dim() else 0
+    a, b = _addr(A, "A", _BF16, lead + (r, d_in), dev), _addr(B, "B", _BF16, lead + (d_out, r), dev)
+    x = _addr(X, "X", _BF16, (M, d_in), dev)
+    if Y is None:
+        Y = torch.empty((M, d_out), dtype=_BF16, device=dev)
+    if not save_t:
+        T = None
+    elif T is None:
+        T = torch.empty((M, r), dtype=_F32, device=dev)
+    y, t = _addr(Y, "Y", _BF16, (M, d_out), dev), _addr(T, "T", _F32, (M, r), dev)
+    ws, nbytes, keep = _ws_args(workspace, need, (M,) + lead + (d_out, d_in, r), dev)
+    _launch(fn, dev, w.struct, *lead, a, b, r, scaling, _dropout(p, rng, dev), x, M, *offsets, y, t, ws, nbytes)
     return Y, T
 
 
-def _group_bwd(call, w, A, B, lead, X, T, dY, p, rng, need_dx, need_da, need_db, dA, dB, accumulate, dX, workspace,
-               need):
-    dev = w.buffer.device
-    d_out, r = _group_shapes(w, A, B, lead)
-    M = dY.shape[0]
-    _matrix(dY, "dY", torch.bfloat16, (M, d_out), dev)
-    _matrix(X, "X", torch.bfloat16, (M, w.d_in), dev)
-    _matrix(T, "T", torch.float32, (M, r), dev)
-    _matrix(dX, "dX", torch.bfloat16, (M, w.d_in), dev)
-    _matrix(dA, "dA", torch.bfloat16, A.shape, dev)
-    _matrix(dB, "dB", torch.bfloat16, B.shape, dev)
+def _group_bwd(fn, need, w, A, B, lead, scaling, X, T, dY, offsets, p, rng, need_dx, need_da, need_db, dA, dB,
+               accumulate, dX, workspace):
+    """Both backwards, as _group_fwd."""
+    dev, d_in = w.buffer.device, w.d_in
+    d_out = w.d_out // lead[0] if lead else w.d_out
+    r = A.shape[-2] if A.dim() == 2 + len(lead) else 0
+    M = dY.shape[0] if dY.dim() else 0
     if accumulate and ((need_da and dA is None) or (need_db and dB is None)):
         raise ValueError("accumulate needs the dA and dB to add to")
-    with torch.cuda.device(dev):
-        dX = (dX if dX is not None else torch.empty((M, w.d_in), dtype=torch.bfloat16, device=dev)) if need_dx else None
-        dA = (dA if dA is not None else torch.empty_like(A)) if need_da else None
-        dB = (dB if dB is not None else torch.empty_like(B)) if need_db else None
-        d = _dropout(p, rng, dev)
-        ws = workspace if workspace is not None else _workspace(need(M, *lead, d_out, w.d_in, r), dev)
-        _check(call(r, ctypes.byref(d), M, dX, dA, dB, 1 if accumulate else 0, ws))
+    a, b = _addr(A, "A", _BF16, lead + (r, d_in), dev), _addr(B, "B", _BF16, lead + (d_out, r), dev)
+    x, t = _addr(X, "X", _BF16, (M, d_in), dev), _addr(T, "T", _F32, (M, r), dev)
+    dy = _addr(dY, "dY", _BF16, (M, d_out), dev)
+    dX = (torch.empty((M, d_in), dtype=_BF16, device=dev) if dX is None else dX) if need_dx else None
+    dA = (torch.empty_like(A) if dA is None else dA) if need_da else None
+    dB = (torch.empty_like(B) if dB is None else dB) if need_db else None
+    dx = _addr(dX, "dX", _BF16, (M, d_in), dev)
+    da, db = _addr(dA, "dA", _BF16, A.shape, dev), _addr(dB, "dB", _BF16, B.shape, dev)
+    ws, nbytes, keep = _ws_args(workspace, need, (M,) + lead + (d_out, d_in, r), dev)
+    _launch(fn, dev, w.struct, *lead, a, b, r, scaling, _dropout(p, rng, dev), x, t, dy, M, *offsets, dx, da, db,
+            1 if accumulate else 0, ws, nbytes)
     return dX, dA, dB
-
-
-def _ws(ws: Optional[torch.Tensor]):
-    return _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()
 
 
 def qlora_linear_dropout_fwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, scaling: float, X: torch.Tensor,
@@ -437,10 +457,8 @@ def qlora_linear_dropout_fwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, sca
     """Y = X W_hat^T + s (D A^T) B^T with D = keep .* X / (1 - p): the layer
     with dropout on the adapter's input.  p and rng as for lora_dropout, which
     drops the same elements of X.  Returns (Y, T), T = s D A^T in fp32."""
-    def call(r, d, M, Y, T, ws):
-        return lib.qlora_linear_dropout_fwd(ctypes.byref(w.struct), _ptr(A), _ptr(B), r, scaling, d, _ptr(X), M,
-                                            _ptr(Y), _ptr(T), *_ws(ws), _stream())
-    return _group_fwd(call, w, A, B, (), X, p, rng, save_t, Y, workspace, T, qlora_linear_dropout_fwd_workspace_bytes)
+    return _group_fwd(lib.qlora_linear_dropout_fwd, qlora_linear_dropout_fwd_workspace_bytes, w, A, B, (), scaling, X,
+                      (), p, rng, save_t, Y, workspace, T)
 
 
 def qlora_linear_dropout_bwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, scaling: float,
@@ -451,18 +469,16 @@ def qlora_linear_dropout_bwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, sca
                              dX: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """(dX, dA, dB) of qlora_linear_dropout_fwd called with the same p and the
     same state in rng; the other arguments as for qlora_linear_bwd."""
-    def call(r, d, M, dX, dA, dB, acc, ws):
-        return lib.qlora_linear_dropout_bwd(ctypes.byref(w.struct), _ptr(A), _ptr(B), r, scaling, d, _ptr(X), _ptr(T),
-                                            _ptr(dY), M, _ptr(dX), _ptr(dA), _ptr(dB), acc, *_ws(ws), _stream())
-    return _group_bwd(call, w, A, B, (), X, T, dY, p, rng, need_dx, need_da, need_db, dA, dB, accumulate, dX, workspace,
-                      qlora_linear_dropout_bwd_workspace_bytes)
+    return _group_bwd(lib.qlora_linear_dropout_bwd, qlora_linear_dropout_bwd_workspace_bytes, w, A, B, (), scaling, X,
+                      T, dY, (), p, rng, need_dx, need_da, need_db, dA, dB, accumulate, dX, workspace)
 
 
-def _experts(w: NF4Tensor, A: torch.Tensor, offsets: torch.Tensor) -> int:
-    if A.dim() != 3 or A.shape[0] < 1 or w.d_out % A.shape[0] != 0:
+def _experts(w: NF4Tensor, A: torch.Tensor, offsets: torch.Tensor):
+    """((n_experts,), (address of the offsets,))."""
+    e = A.shape[0] if A.dim() == 3 else 0
+    if e < 1 or w.d_out % e != 0:
         raise ValueError("A must be [n_experts, r, d_in], and the weight's %d rows n_experts times d_out" % w.d_out)
-    _matrix(offsets, "offsets", torch.int32, (A.shape[0] + 1,), w.buffer.device)
-    return A.shape[0]
+    return (e,), (_addr(offsets, "offsets", torch.int32, (e + 1,), w.buffer.device),)
 
 
 def qlora_grouped_fwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, scaling: float, X: torch.Tensor,
@@ -476,12 +492,9 @@ def qlora_grouped_fwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, scaling: f
     (Y, T); rows outside the groups keep what Y and T held, which is nothing in
     particular where they are allocated here.  p and rng: dropout on the
     adapter's input, as for qlora_linear_dropout_fwd."""
-    e = _experts(w, A, offsets)
-
-    def call(r, d, M, Y, T, ws):
-        return lib.qlora_grouped_fwd(ctypes.byref(w.struct), e, _ptr(A), _ptr(B), r, scaling, d, _ptr(X), M,
-                                     _ptr(offsets), _ptr(Y), _ptr(T), *_ws(ws), _stream())
-    return _group_fwd(call, w, A, B, (e,), X, p, rng, save_t, Y, workspace, T, qlora_grouped_fwd_workspace_bytes)
+    lead, off = _experts(w, A, offsets)
+    return _group_fwd(lib.qlora_grouped_fwd, qlora_grouped_fwd_workspace_bytes, w, A, B, lead, scaling, X, off, p, rng,
+                      save_t, Y, workspace, T)
 
 
 def qlora_grouped_bwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, scaling: float, X: Optional[torch.Tensor],
@@ -493,14 +506,9 @@ def qlora_grouped_bwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, scaling: f
     """(dX, dA, dB) of qlora_grouped_fwd called with the same offsets, p and
     state in rng; dA [n_experts, r, d_in] and dB [n_experts, d_out, r] are zero
     for an expert without rows.  The other arguments as for qlora_linear_bwd."""
-    e = _experts(w, A, offsets)
-
-    def call(r, d, M, dX, dA, dB, acc, ws):
-        return lib.qlora_grouped_bwd(ctypes.byref(w.struct), e, _ptr(A), _ptr(B), r, scaling, d, _ptr(X), _ptr(T),
-                                     _ptr(dY), M, _ptr(offsets), _ptr(dX), _ptr(dA), _ptr(dB), acc, *_ws(ws),
-                                     _stream())
-    return _group_bwd(call, w, A, B, (e,), X, T, dY, p, rng, need_dx, need_da, need_db, dA, dB, accumulate, dX,
-                      workspace, qlora_grouped_bwd_workspace_bytes)
+    lead, off = _experts(w, A, offsets)
+    return _group_bwd(lib.qlora_grouped_bwd, qlora_grouped_bwd_workspace_bytes, w, A, B, lead, scaling, X, T, dY, off,
+                      p, rng, need_dx, need_da, need_db, dA, dB, accumulate, dX, workspace)
 
 
 def nf4_merge_workspace_bytes(d_out: int, d_in: int) -> int:

@@ -143,6 +143,8 @@ struct Split {
 // `steps` split into parts of at least four steps so that tiles x parts is
 // about `ctas`; no part is empty.
 Split split_steps(int64_t tiles, int64_t steps, int ctas) {
+    // a few steps are over before a second kernel could add their parts
+    if (steps <= 8) return {1, static_cast<int>(steps)};
     int64_t s = std::max<int64_t>(1, (ctas + tiles / 2) / std::max<int64_t>(1, tiles));
     s = std::min(s, std::max<int64_t>(1, steps / 4));
     const int64_t per = div_up(steps, s);
@@ -178,7 +180,7 @@ int64_t most_partials(int E, int64_t M, int part_steps) {
 // a split contraction the partials' way through memory and one more kernel).
 // The groups are taken as equal, which the host has to.
 struct FusedPlan {
-    bool few;       // 32-token tiles, two CTAs per SM, steps of 128; else up to 512 tokens, one, of 64
+    bool few;       // 32-token tiles, two CTAs per SM; else up to 512 tokens, one CTA
     int tile_rows;
     int splits;
     int k_main, k_ext;  // steps
@@ -200,7 +202,7 @@ FusedPlan plan_fused(int E, int64_t M, int64_t cols, int64_t contraction, int r,
         const int most = best.few ? 8 : static_cast<int>(std::min<int64_t>(8, pairs / tiles));
         for (int splits = 1; splits <= std::max(1, most) && (splits == 1 || splits * 4 <= best.k_main); ++splits) {
             const double rounds = static_cast<double>(div_up(tiles * splits, pairs));
-            const double step = best.few ? 1400.0 : std::max(2.1 * size + 250.0, 500.0);
+            const double step = best.few ? 1500.0 : std::max(2.1 * size + 250.0, 500.0);
             double cost = rounds * (step * static_cast<double>(div_up(best.k_main, splits) + best.k_ext) + 3000.0 +
                                     16.0 * size);
             if (splits > 1) cost += 6000.0 + static_cast<double>(splits) * M * cols * 8 / 2000.0;
@@ -318,10 +320,16 @@ int rank_rows(const GroupCtx& c, bool is_t, const uint16_t* act, const uint16_t*
     if (is_t ? !map16(&mb, factor, c.K, c.r, c.E, g.rn) : !map16(&mb, factor, ceil_to(c.r, 8), c.N, c.E, 64)) return -1;
     const dim3 grid(static_cast<unsigned>(most_tiles(c.offsets, c.E, c.M, 128)), 1, sp.splits);
     const bool drop = is_t && c.drop.threshold != 0;
+    g.alpha = drop ? c.s * c.drop.gain : c.s;
+    if (sp.splits == 1) {
+        g.pair = pair;
+        g.out32 = out32;
+    }
     const cudaError_t e = drop   ? launch_rank<RANK_T, true>("rank_t_drop", ma, mb, g, grid, c.stream)
                           : is_t ? launch_rank<RANK_T, false>("rank_t", ma, mb, g, grid, c.stream)
                                  : launch_rank<RANK_V, false>("rank_v", ma, mb, g, grid, c.stream);
     if (e != cudaSuccess) return -2;
+    if (sp.splits == 1) return 0;
     RankRowsSumArgs s{};
     s.offsets = c.offsets;
     s.E = c.E;
@@ -332,11 +340,10 @@ int rank_rows(const GroupCtx& c, bool is_t, const uint16_t* act, const uint16_t*
     s.r = c.r;
     s.rn = g.rn;
     s.r64 = g.r64;
-    s.alpha = drop ? c.s * c.drop.gain : c.s;
+    s.alpha = g.alpha;
     s.pair = pair;
     s.out32 = out32;
-    s.check = 1;
-    return launch_dependent("rank_sum", k_rank_rows_sum, flat_grid(c.M * (g.r64 / 4), c.num_sms), 256, 0, c.stream,
+    return launch_dependent("rank_sum", k_rank_rows_sum, flat_grid(c.M * (g.r64 / 8), c.num_sms), 256, 0, c.stream,
                             s) == cudaSuccess ? 0 : -2;
 }
 
@@ -403,6 +410,10 @@ cudaError_t launch_group_gemm(const char* name, FusedMaps& f, GroupGemmArgs g, b
     // one CTA (or two) on every SM, each pair walking its share of the tiles
     const int64_t pairs =
         std::min<int64_t>(num_sms / 2 * C::kMinBlocks, row_tiles * g.col_tiles * g.splits);
+    const int fast = g.row_tiles >= 0 ? g.row_tiles : g.col_tiles;
+    g.walk_z = static_cast<int>(pairs % g.splits);
+    g.walk_fast = static_cast<int>(pairs / g.splits % fast);
+    g.walk_slow = static_cast<int>(pairs / g.splits / fast);
     const dim3 grid(static_cast<unsigned>(2 * pairs));
     return launch_clustered(name, k_group_gemm<DX, T, DROP>, grid, 2, C::kThreads, C::kSmem, st, f.m[0], f.m[1],
                             f.m[2], f.m[3], g);
@@ -522,7 +533,7 @@ int group_bwd(const GroupCtx& c, const uint16_t* A, const uint16_t* B, const uin
             rc = rank_rows(c, true, X, A, w.T2, nullptr, w.part);
         } else {
             const int r64 = rank64(c.r);
-            if (launch_dependent("rank_pair", k_rank_pair, flat_grid(c.M * r64, c.num_sms), 256, 0, c.stream, T_saved,
+            if (launch_dependent("rank_pair", k_rank_pair, flat_grid(c.M * (r64 / 8), c.num_sms), 256, 0, c.stream, T_saved,
                                  c.M, c.r, r64, w.T2) != cudaSuccess)
                 rc = -2;
         }

@@ -76,6 +76,12 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // 32 lanes x 8 columns of fp32.
 __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -99,18 +105,19 @@ __device__ __forceinline__ void group_bounds(const int32_t* offsets, int e, int 
 
 // Tile t of all groups' tiles of at most `most` rows, in group order; the whole
 // warp calls it.  EVEN: a group's tiles are of one size, a multiple of 32, else
-// all but its last have `most` rows.  False beyond the last tile.
-template <bool EVEN>
-__device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int M, int most, int t, int lane,
+// all but its last have `most` rows.  bounds(e, begin, end) gives a group's rows.
+// False beyond the last tile.
+template <bool EVEN, typename Bounds>
+__device__ __forceinline__ bool find_tile(bool grouped, const Bounds& bounds, int E, int M, int most, int t, int lane,
                                           GroupTile& g) {
     int begin = 0, end = M, first = 0;
     g.e = 0;
-    if (offsets != nullptr) {
+    if (grouped) {
         bool found = false;
         for (int e0 = 0; e0 < E && !found; e0 += 32) {
             const int e = e0 + lane;
             begin = end = 0;
-            if (e < E) group_bounds(offsets, e, M, begin, end);
+            if (e < E) bounds(e, begin, end);
             const int n = (end - begin + most - 1) / most;
             int incl = n;
 #pragma unroll
@@ -140,6 +147,14 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int M, 
     g.row0 = begin + (t - first) * size;
     g.row_end = EVEN ? min(end, g.row0 + size) : end;
     return g.row0 < end;
+}
+
+// The same with the bounds from device memory.
+template <bool EVEN>
+__device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int M, int most, int t, int lane,
+                                          GroupTile& g) {
+    auto bounds = [&](int e, int& begin, int& end) { group_bounds(offsets, e, M, begin, end); };
+    return find_tile<EVEN>(offsets != nullptr, bounds, E, M, most, t, lane, g);
 }
 
 // ------------------------------------------------------------------ one thread of a warp
@@ -184,6 +199,19 @@ __device__ __forceinline__ void mma2_elect(uint32_t d_tmem, uint64_t a_desc, uin
         "setp.ne.b32 p, %4, 0;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// The same with operand A in tensor memory: 128 lanes (rows) of each CTA by 8
+// columns, two bf16 of the contraction in a column.
+__device__ __forceinline__ void mma2_elect_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -236,6 +264,19 @@ __device__ __forceinline__ void tmem2_dealloc(uint32_t taddr, uint32_t ncols) {
 // selectors formed for a whole code word; the byte permutes and logic run on the
 // integer pipe at half rate and are what the decode is bound by, so the shifts
 // are written as high halves of products, which run on the multiply pipe.
+__device__ __forceinline__ void decode_word(uint32_t w, const uint32_t (&P)[4], const uint32_t (&H)[4], uint32_t* o) {
+    const uint32_t sel = w & 0x77777777u;                                          // index within 0-7 / 8-15
+    const uint32_t pick = (__umulhi(w, 0x80000000u) & 0x44444444u) | 0x32103210u;  // from 8-15 if bit 3
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t se = h ? __umulhi(sel, 0x10000u) : sel, pk = h ? __umulhi(pick, 0x10000u) : pick;
+        const uint32_t lo = __byte_perm(__byte_perm(P[0], P[1], se), __byte_perm(P[2], P[3], se), pk);
+        const uint32_t hi = __byte_perm(__byte_perm(H[0], H[1], se), __byte_perm(H[2], H[3], se), pk);
+        o[2 * h] = __byte_perm(lo, hi, 0x4051);
+        o[2 * h + 1] = __byte_perm(lo, hi, 0x6273);
+    }
+}
+
 __device__ __forceinline__ void decode_row(const uint8_t* src, float s, uint8_t* dst) {
     uint32_t P[4], H[4];
     nf4_table(s, P, H);
@@ -245,21 +286,36 @@ __device__ __forceinline__ void decode_row(const uint8_t* src, float s, uint8_t*
     const uint32_t at = smem_u32(dst);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const uint32_t w = words[j];
-        const uint32_t sel = w & 0x77777777u;                                     // index within 0-7 / 8-15
-        const uint32_t pick = (__umulhi(w, 0x80000000u) & 0x44444444u) | 0x32103210u;  // from 8-15 if bit 3
         uint32_t o[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t se = h ? __umulhi(sel, 0x10000u) : sel, pk = h ? __umulhi(pick, 0x10000u) : pick;
-            const uint32_t lo = __byte_perm(__byte_perm(P[0], P[1], se), __byte_perm(P[2], P[3], se), pk);
-            const uint32_t hi = __byte_perm(__byte_perm(H[0], H[1], se), __byte_perm(H[2], H[3], se), pk);
-            o[2 * h] = __byte_perm(lo, hi, 0x4051);
-            o[2 * h + 1] = __byte_perm(lo, hi, 0x6273);
-        }
+        decode_word(words[j], P, H, o);
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (j << 4)), "r"(o[0]), "r"(o[1]), "r"(o[2]),
                      "r"(o[3])
                      : "memory");
+    }
+}
+
+// The same unit into tensor memory: 32 columns of the thread's lane from `taddr`
+// on (the warp's lane base in it), two weights a column; the whole warp calls it,
+// and waits for the stores itself.  The look-up is a shuffle from the lane that
+// holds the level (`level`: of this lane's index modulo 16), which needs no table
+// and no logic: 252 clocks per SM for the units of four warps, where byte permutes
+// take 370 (and look-ups in shared memory 293); mixtures lie in between.
+__device__ __forceinline__ void decode_lane(const uint8_t* src, float s, float level, uint32_t taddr) {
+    const uint4 c0 = *reinterpret_cast<const uint4*>(src);
+    const uint4 c1 = *reinterpret_cast<const uint4*>(src + 16);
+    const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w = words[j + i / 4];
+            const int b = 8 * (i % 4);
+            const float even = __shfl_sync(0xFFFFFFFFu, level, w >> (b + 4), 16);
+            const float odd = __shfl_sync(0xFFFFFFFFu, level, w >> b, 16);
+            o[i] = pack_bf16x2(__fmul_rn(even, s), __fmul_rn(odd, s));
+        }
+        tmem_st_32x32b_x8(taddr + 4 * j, o);
     }
 }
 
@@ -275,6 +331,7 @@ struct GroupGemmArgs {
     int tile_rows;           // at most, a multiple of 32
     int col_tiles;
     int row_tiles;           // walked first when >= 0 (one dense group, its exact count), else the column tiles are
+    int walk_z, walk_fast, walk_slow;  // number of pairs = walk_z + splits (walk_fast + fast tiles walk_slow)
     // encoded weight: rows and blocks of one expert
     const int8_t* qscale;
     const float* scale2;
@@ -287,34 +344,46 @@ struct GroupGemmArgs {
     DropArgs drop;           // input gradient with dropout only
 };
 
-// T tokens per tile at most.  512: one CTA per SM, four teams, steps of 64; 32:
-// two CTAs per SM of two teams each, whose starts and ends overlap, and steps of
-// 128 (kKS = 2 units per thread), which halve the barrier waits per decoded
-// weight where the decode is what takes the time.
+// T tokens per tile at most.  512: one CTA per SM, four teams, steps of 64; the
+// MMAs bound it.  32: the decode bounds it, so two CTAs per SM of two teams each,
+// whose starts and ends overlap, and steps of 128 (kKS = 2 units per thread),
+// which halve the waits, arrivals and turns of the copying and issuing warps per
+// decoded weight (steps of 64: 167 us for 64 tokens over eight experts of
+// 4096 x 11008, steps of 128: 143 us).  Forward (kWT): the tile is K-major, lane =
+// weight row, and goes to tensor memory (32 columns a unit; three steps fit beside
+// the accumulators), by which the shared-memory pipe is free to do the look-ups as
+// shuffles (decode_lane): 107-112 us.  Input gradient: the tile is MN-major, which
+// only shared memory can hold.
 template <bool DX, int T>
 struct GroupGemmConfig {
     static constexpr int kBM = 128;                    // weight columns of one CTA
     static constexpr int kSubs = T > 256 ? 2 : 1;      // accumulators
     static constexpr int kSubT = T / kSubs;            // tokens of one, half of them per CTA
+    static constexpr bool kWT = T <= 64 && !DX;
     static constexpr int kTeams = T > 64 ? 4 : 2;
-    static constexpr int kKS = T > 64 ? 1 : 2;         // 64s of the contraction in a step
-    static constexpr int kDS = T > 64 ? 4 : 2;         // slots of decoded tiles and of tokens
+    static constexpr int kKS = T > 64 ? 1 : 2;  // 64s of the contraction in a step
+    static constexpr int kDS = T > 64 ? 4 : kWT ? 3 : 2;  // slots of decoded tiles and of tokens
     static constexpr int kLC = 2 * kDS;                // slots of packed codes
+    static constexpr int kWS = kWT ? 1 : kDS;          // slots of weight tiles in shared memory (kWT: extension only)
     static constexpr int kSub = kSubT / 2 * 128;       // a CTA's tokens of one accumulator, 64 deep
     static constexpr int kTok = kSubs * kSub;          // of all accumulators
     static constexpr int kCodes = kBM * 32, kW = kBM * 128;  // a packed and a decoded tile, 64 deep
     static constexpr int kTokBytes = kKS * kTok, kCBytes = kKS * kCodes, kWBytes = kKS * kW;
-    static constexpr int kSmem = kDS * (kTokBytes + kWBytes) + kLC * kCBytes + 1024;
+    static constexpr int kSmem = kDS * kTokBytes + kWS * kWBytes + kLC * kCBytes + 1024;
     static constexpr int kTeamThreads = kBM;           // one (row, block) unit each
     static constexpr int kTeamWarps = kTeamThreads / 32;
     static constexpr int kWorkWarps = kTeamWarps * kTeams;
     static constexpr int kThreads = 64 + 32 * kWorkWarps;
     static constexpr int kMinBlocks = T > 64 ? 1 : 2;
-    static constexpr int kTmemCols = T < 32 ? 32 : T;
+    static constexpr int kAccs = T > 64 || kWT ? 1 : 2;       // accumulator sets: the next tile's MMAs run beside the epilogue
+    static constexpr int kAccCols = T;                 // columns of a set
+    static constexpr int kTmemCols = kWT ? 256 : kAccs * T;
     static constexpr uint32_t kIdesc = make_idesc_bf16(2 * kBM, 0, DX ? 1 : 0, 0);  // without N
-    // a wait for a barrier's phase is sound only where the phase before it is
-    // known to be complete: a slot is always the same team's
-    static_assert(kDS % kTeams == 0 && kLC % kTeams == 0 && kLC >= kDS, "rings");
+    // A wait for a barrier's phase is sound only where the phase before it is
+    // known to be complete: a slot is always the same team's, or (three slots) that
+    // phase belongs to a step whose successor this team has seen multiplied.
+    static_assert((kDS % kTeams == 0 || kDS == kTeams + 1) && kLC % kTeams == 0 && kLC >= kDS, "rings");
+    static_assert(!kWT || kAccs * T + kDS * kKS * 32 <= kTmemCols, "tensor memory");
     static_assert(kSub % 1024 == 0 && kSmem * kMinBlocks <= 226 * 1024, "shared memory");
 };
 
@@ -335,9 +404,15 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
     // bar_ready, bar_masked and bar_free count both CTAs, in the leading one
     // (rank 0); the MMAs' completions (bar_done, bar_accum, bar_ext) arrive in
     // both; bar_codes is each CTA's own
-    __shared__ uint64_t bar_codes[LC], bar_ready[DS], bar_done[DS], bar_accum, bar_ext, bar_masked, bar_free;
+    __shared__ uint64_t bar_codes[LC], bar_ready[DS], bar_done[DS], bar_accum[C::kAccs], bar_ext, bar_masked,
+        bar_free[C::kAccs];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
+    // The groups' rows, first tiles and tile sizes, worked out once; for more
+    // groups than this a warp scans the offsets for every tile.
+    constexpr int kGroups = 127;
+    __shared__ int s_off[kGroups + 1], s_first[kGroups + 1];
+    __shared__ uint16_t s_size[kGroups + 1];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
@@ -356,23 +431,59 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
         int nsub;
         int z, kb0, n_main, n_ext;
     };
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    auto next_tile = [&](int tl, Tile& t) {
-        int i = pair + tl * pairs;
-        t.z = 0;
-        if (args.splits > 1) {
-            t.z = i % args.splits;
-            i /= args.splits;
+    const bool kept = args.offsets != nullptr && args.E <= kGroups;
+    // The walk over this pair's tiles: tile i = pair + tl pairs is split z of
+    // column tile ct and token tile rt, kept as running numbers (the steps of a
+    // walk, pairs = dct + col_tiles (drt + ...), come from the host: a division
+    // costs as much as a good part of a decode).
+    struct Walk {
+        int z, fast, slow;
+    };
+    const int fast_n = args.row_tiles >= 0 ? args.row_tiles : args.col_tiles;
+    auto first_tile = [&](Walk& w) {
+        const int i = blockIdx.x >> 1;
+        w.z = i % args.splits;
+        w.fast = i / args.splits % fast_n;
+        w.slow = i / args.splits / fast_n;
+    };
+    auto next_tile = [&](Walk& w, Tile& t) {
+        t.z = w.z;
+        const int ct = args.row_tiles >= 0 ? w.slow : w.fast, rt = args.row_tiles >= 0 ? w.fast : w.slow;
+        w.z += args.walk_z;
+        w.fast += args.walk_fast;
+        w.slow += args.walk_slow;
+        if (w.z >= args.splits) {
+            w.z -= args.splits;
+            ++w.fast;
         }
-        const int ct = args.row_tiles >= 0 ? i / args.row_tiles : i % args.col_tiles;
-        const int rt = args.row_tiles >= 0 ? i % args.row_tiles : i / args.col_tiles;
-        if (ct >= args.col_tiles || !find_tile<true>(args.offsets, args.E, args.M, args.tile_rows, rt, lane, t.g))
+        if (w.fast >= fast_n) {
+            w.fast -= fast_n;
+            ++w.slow;
+        }
+        if (ct >= args.col_tiles) return false;
+        if (kept) {
+            // the last group whose first tile is not beyond rt (groups without rows
+            // share their first tile with the next one)
+            int e = -1;
+            for (int e0 = 0; e0 < args.E; e0 += 32)
+                e += __popc(__ballot_sync(0xFFFFFFFFu, e0 + lane < args.E && s_first[min(e0 + lane, kGroups)] <= rt));
+            if (rt >= s_first[args.E]) return false;
+            const int begin = min(max(s_off[e], 0), args.M);
+            t.g.e = e;
+            t.g.row0 = begin + (rt - s_first[e]) * s_size[e];
+            t.g.row_end = min(min(max(s_off[e + 1], begin), args.M), t.g.row0 + s_size[e]);
+        } else if (!find_tile<true>(args.offsets, args.E, args.M, args.tile_rows, rt, lane, t.g)) {
             return false;
+        }
         t.h0 = (2 * ct + rank) * C::kBM;
         t.tokens = t.g.row_end - t.g.row0;
         t.nsub = C::kSubs == 2 && t.tokens > C::kSubT ? 2 : 1;
-        t.kb0 = static_cast<int>(static_cast<int64_t>(args.k_main) * t.z / args.splits);
-        t.n_main = static_cast<int>(static_cast<int64_t>(args.k_main) * (t.z + 1) / args.splits) - t.kb0;
+        t.kb0 = 0;
+        t.n_main = args.k_main;
+        if (args.splits > 1) {
+            t.kb0 = args.k_main * t.z / args.splits;
+            t.n_main = args.k_main * (t.z + 1) / args.splits - t.kb0;
+        }
         t.n_ext = t.z == 0 ? args.k_ext : 0;
         return true;
     };
@@ -384,10 +495,11 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
 
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-    // buffers of running step gi (counted over the pair's tiles), code slot cs
-    auto t_buf = [&](int gi) { return base + (gi % DS) * C::kTokBytes; };
-    auto w_buf = [&](int gi) { return base + DS * C::kTokBytes + (gi % DS) * C::kWBytes; };
-    auto codes_buf = [&](int cs) { return base + DS * (C::kTokBytes + C::kWBytes) + cs * C::kCBytes; };
+    // Buffers: a step's slot ds, code slot cs, and its weight slot: ds, or with the
+    // decoded tiles in tensor memory the extension steps' own two
+    auto t_buf = [&](int ds) { return base + ds * C::kTokBytes; };
+    auto w_buf = [&](int ws) { return base + DS * C::kTokBytes + ws * C::kWBytes; };
+    auto codes_buf = [&](int cs) { return base + DS * C::kTokBytes + C::kWS * C::kWBytes + cs * C::kCBytes; };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < LC; ++i) mbar_init(&bar_codes[i], 1);
@@ -395,12 +507,35 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             mbar_init(&bar_ready[i], 1 + 2 * C::kTeamWarps);
             mbar_init(&bar_done[i], 1);
         }
-        mbar_init(&bar_accum, 1);
+        for (int i = 0; i < C::kAccs; ++i) {
+            mbar_init(&bar_accum[i], 1);
+            mbar_init(&bar_free[i], 2 * C::kWorkWarps);
+        }
         mbar_init(&bar_ext, 1);
         mbar_init(&bar_masked, 2 * C::kWorkWarps);
-        mbar_init(&bar_free, 2 * C::kWorkWarps);
         s_abort = 0;
         fence_barrier_init();
+    }
+    if (kept && warp == 1) {
+        int tiles = 0;
+        for (int e0 = 0; e0 <= args.E; e0 += 32) {
+            const int e = e0 + lane;
+            int begin = 0, end = 0;
+            if (e < args.E) group_bounds(args.offsets, e, args.M, begin, end);
+            const int n = end - begin, k = (n + args.tile_rows - 1) / args.tile_rows;
+            int incl = k;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+                if (lane >= d) incl += v;
+            }
+            if (e <= args.E) {
+                s_off[e] = __ldcg(args.offsets + e);
+                s_first[e] = tiles + incl - k;
+                s_size[e] = static_cast<uint16_t>(k > 0 ? ((n + k - 1) / k + 31) & ~31 : 0);
+            }
+            tiles += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        }
     }
     // both CTAs' barriers are initialised once this barrier is passed
     cluster_arrive_release();
@@ -418,73 +553,83 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             tma_prefetch_desc(&map_we);
         }
         __syncwarp();
-        int gi = 0;
         bool waited = false;
         // the codes run kAhead steps before the tokens, into the next tile
         constexpr int kAhead = LC - DS;
         Tile tc, tt;  // tiles of the codes' and of the tokens' step
-        int tlc = 0, itc = 0, cs = 0;
-        bool have_c = next_tile(0, tc);
+        Walk wc, wt;
+        first_tile(wc);
+        wt = wc;
+        int itc = 0, csc = 0;
+        bool have_c = next_tile(wc, tc);
         // packed codes of step itc, or nothing on an extension step, whose factor
         // tile goes with its tokens
         auto codes_step = [&]() {
             if (!have_c) return;
             if (is_main(tc, itc) && elect_one()) {
-                uint64_t* bar = &bar_codes[cs];
+                uint64_t* bar = &bar_codes[csc];
                 mbar_arrive_expect_tx(bar, C::kCBytes);
                 const int kb = (tc.kb0 + itc - main0(tc)) * C::kKS;
 #pragma unroll
                 for (int h = 0; h < C::kKS; ++h) {
-                    uint8_t* dst = codes_buf(cs) + h * C::kCodes;
+                    uint8_t* dst = codes_buf(csc) + h * C::kCodes;
                     if constexpr (DX) tma_load_3d(dst, &map_w, bar, tc.h0 / 2, (kb + h) * 64, tc.g.e);
                     else tma_load_3d(dst, &map_w, bar, (kb + h) * 32, tc.h0, tc.g.e);
                 }
             }
             __syncwarp();
-            if (++cs == LC) cs = 0;
+            if (++csc == LC) csc = 0;
             if (++itc == tc.n_main + tc.n_ext) {
                 itc = 0;
-                have_c = next_tile(++tlc, tc);
+                have_c = next_tile(wc, tc);
             }
         };
         for (int i = 0; i < kAhead; ++i) codes_step();
-        int ws = 0;  // code slot of step gi
+        int ds = 0, cs = 0;     // slots of the tokens' step
+        uint32_t done = 0;      // parity of the round over the slots
+        bool used = false;      // every slot has been used
         bool stop = false;
-        for (int tl = 0; !stop && next_tile(tl, tt); ++tl) {
+        while (!stop && next_tile(wt, tt)) {
             const int n_iter = tt.n_main + tt.n_ext;
-            for (int it = 0; it < n_iter; ++it, ++gi) {
-                // step gi - DS is multiplied: its token and decode slots are free,
-                // and so is the code slot of step gi + kAhead, which its decode has
-                // read.  The warp stays together also when a wait gives up.
-                stop = __any_sync(0xFFFFFFFFu,
-                                  (gi >= DS && !mbar_wait(&bar_done[gi % DS], ((gi / DS) & 1u) ^ 1u, abort_flag)) ||
-                                      *abort_flag);
+            for (int it = 0; it < n_iter; ++it) {
+                // the step DS before is multiplied: its token and decode slots are
+                // free, and so is the code slot of the step kAhead ahead, which its
+                // decode has read.  The warp stays together also when a wait gives up.
+                stop = __any_sync(0xFFFFFFFFu, (used && !mbar_wait(&bar_done[ds], done ^ 1u, abort_flag)) || *abort_flag);
                 if (stop) break;
+                const bool main_step = is_main(tt, it);
+                const int j0 = (DROP ? it : it - tt.n_main) * C::kKS;  // of an extension step
+                if (C::kWT && !main_step && j0 >= C::kWS) {
+                    // the step that read this extension slot last, kWS before this one
+                    const int back = ds >= C::kWS ? ds - C::kWS : ds - C::kWS + DS;
+                    const uint32_t parity = ds >= C::kWS ? done : done ^ 1u;
+                    stop = __any_sync(0xFFFFFFFFu, !mbar_wait(&bar_done[back], parity, abort_flag));
+                    if (stop) break;
+                }
                 if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(&bar_ready[gi % DS], 2 * C::kKS * tt.nsub * C::kSub);
-                    const uint32_t bar = lead(&bar_ready[gi % DS]);
-                    if (is_main(tt, it)) {
+                    if (rank == 0) mbar_arrive_expect_tx(&bar_ready[ds], 2 * C::kKS * tt.nsub * C::kSub);
+                    const uint32_t bar = lead(&bar_ready[ds]);
+                    if (main_step) {
                         const int kb = (tt.kb0 + it - main0(tt)) * C::kKS;
 #pragma unroll
                         for (int h = 0; h < C::kKS; ++h)
                             for (int ms = 0; ms < tt.nsub; ++ms)
-                                tma_load_2d_pair(t_buf(gi) + h * C::kTok + ms * C::kSub, &map_t, bar, (kb + h) * 64,
+                                tma_load_2d_pair(t_buf(ds) + h * C::kTok + ms * C::kSub, &map_t, bar, (kb + h) * 64,
                                                  sub_row(tt, ms));
                     } else {
-                        // [hi | lo] against the factor twice; the factor's tile
-                        // lands in the decode slot
-                        const int j0 = (DROP ? it : it - tt.n_main) * C::kKS, half = tt.n_ext * C::kKS / 2;
+                        // [hi | lo] against the factor twice
+                        const int half = tt.n_ext * C::kKS / 2;
                         if (!waited) grid_dependency_wait();
                         waited = true;
-                        uint64_t* wbar = &bar_codes[ws];
+                        uint64_t* wbar = &bar_codes[cs];
                         mbar_arrive_expect_tx(wbar, C::kWBytes);
 #pragma unroll
                         for (int h = 0; h < C::kKS; ++h) {
                             const int j = j0 + h, jb = j % half;
                             for (int ms = 0; ms < tt.nsub; ++ms)
-                                tma_load_2d_pair(t_buf(gi) + h * C::kTok + ms * C::kSub, &map_te, bar, j * 64,
+                                tma_load_2d_pair(t_buf(ds) + h * C::kTok + ms * C::kSub, &map_te, bar, j * 64,
                                                  sub_row(tt, ms));
-                            uint8_t* dst = w_buf(gi) + h * C::kW;
+                            uint8_t* dst = w_buf(C::kWT ? j0 % C::kWS : ds) + h * C::kW;
                             if constexpr (DX) {
 #pragma unroll
                                 for (int c = 0; c < C::kBM / 64; ++c)
@@ -496,7 +641,12 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                     }
                 }
                 __syncwarp();
-                if (++ws == LC) ws = 0;
+                if (++cs == LC) cs = 0;
+                if (++ds == DS) {
+                    ds = 0;
+                    done ^= 1u;
+                    used = true;
+                }
                 codes_step();
             }
         }
@@ -522,45 +672,65 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             // uniform registers and an MMA costs a few clocks to issue.
             const uint32_t tmem_d = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
             bool stop = false;
-            int gi = 0, n_masked = 0;
+            int n_masked = 0, ds = 0;
+            uint32_t ready = 0;
+            Walk walk;
+            first_tile(walk);
             const uint64_t w_desc0 = tile_desc(smem_u32(w_buf(0)), DX, 0);
             const uint64_t t_desc0 = tile_desc(smem_u32(t_buf(0)), false, 0);
             constexpr uint32_t kWk = DX ? 2048 / 16 : 32 / 16, kTk = 32 / 16;  // next 16 of the contraction
             for (int tl = 0; !stop; ++tl) {
                 Tile t;
-                if (!next_tile(tl, t)) break;
+                if (!next_tile(walk, t)) break;
                 const int nsub = __shfl_sync(0xFFFFFFFFu, t.nsub, 0);
+                const int n_main = __shfl_sync(0xFFFFFFFFu, t.n_main, 0);
                 const int n_iter = __shfl_sync(0xFFFFFFFFu, t.n_main + t.n_ext, 0);
                 const int ext_last = DROP ? __shfl_sync(0xFFFFFFFFu, t.n_ext, 0) - 1 : -1;
                 const uint32_t idesc0 = __shfl_sync(
                     0xFFFFFFFFu, C::kIdesc | (static_cast<uint32_t>(max(32, sub_n(t, 0)) >> 3) << 17), 0);
                 const uint32_t idesc1 = __shfl_sync(
                     0xFFFFFFFFu, C::kIdesc | (static_cast<uint32_t>(max(32, sub_n(t, 1)) >> 3) << 17), 0);
-                // the last tile's accumulators have been read
-                if (tl > 0) stop = !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_free, (tl - 1) & 1u, abort_flag));
-                for (int it = 0; it < n_iter && !stop; ++it, ++gi) {
+                // the accumulators of the last tile that had them have been read
+                const uint32_t acc_d = tmem_d + (C::kAccs == 2 ? (tl & 1) * C::kAccCols : 0);
+                if (tl >= C::kAccs)
+                    stop = !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_free[tl % C::kAccs], (tl / C::kAccs + 1) & 1u,
+                                                              abort_flag));
+                for (int it = 0; it < n_iter && !stop; ++it) {
                     // the tokens and the weight tiles of both CTAs are in place
-                    stop = !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_ready[gi % DS], (gi / DS) & 1u, abort_flag));
+                    stop = !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_ready[ds], ready, abort_flag));
                     if (stop) break;
                     tc_fence_after();
-                    const uint64_t wd = w_desc0 + static_cast<uint32_t>(gi % DS) * (C::kWBytes / 16);
-                    const uint64_t td = t_desc0 + static_cast<uint32_t>(gi % DS) * (C::kTokBytes / 16);
+                    const uint64_t td = t_desc0 + static_cast<uint32_t>(ds) * (C::kTokBytes / 16);
                     const uint32_t acc = it > 0 ? 1u : 0u;
+                    if (C::kWT && it < n_main) {
+                        const uint32_t wt = tmem_d + C::kAccs * C::kAccCols + ds * (32 * C::kKS);
 #pragma unroll
-                    for (int k = 0; k < 4 * C::kKS; ++k) {
-                        const uint64_t w16 = wd + (k / 4) * (C::kW / 16) + (k % 4) * kWk;
-                        const uint64_t t16 = td + (k / 4) * (C::kTok / 16) + (k % 4) * kTk;
-                        mma2_elect(tmem_d, w16, t16, idesc0, k > 0 ? 1u : acc);
-                        if (C::kSubs == 2 && nsub == 2)
-                            mma2_elect(tmem_d + C::kSubT, w16, t16 + C::kSub / 16, idesc1, k > 0 ? 1u : acc);
+                        for (int k = 0; k < 4 * C::kKS; ++k)
+                            mma2_elect_ts(acc_d, wt + 8 * k, td + (k / 4) * (C::kTok / 16) + (k % 4) * kTk, idesc0,
+                                          k > 0 ? 1u : acc);
+                    } else {
+                        const int ws = C::kWT ? (it - n_main) % C::kWS : ds;
+                        const uint64_t wd = w_desc0 + static_cast<uint32_t>(ws) * (C::kWBytes / 16);
+#pragma unroll
+                        for (int k = 0; k < 4 * C::kKS; ++k) {
+                            const uint64_t w16 = wd + (k / 4) * (C::kW / 16) + (k % 4) * kWk;
+                            const uint64_t t16 = td + (k / 4) * (C::kTok / 16) + (k % 4) * kTk;
+                            mma2_elect(acc_d, w16, t16, idesc0, k > 0 ? 1u : acc);
+                            if (C::kSubs == 2 && nsub == 2)
+                                mma2_elect(acc_d + C::kSubT, w16, t16 + C::kSub / 16, idesc1, k > 0 ? 1u : acc);
+                        }
                     }
-                    mma2_commit_elect(&bar_done[gi % DS]);
+                    mma2_commit_elect(&bar_done[ds]);
                     if (DROP && it == ext_last) {
                         mma2_commit_elect(&bar_ext);
                         stop = !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_masked, n_masked++ & 1u, abort_flag));
                     }
+                    if (++ds == DS) {
+                        ds = 0;
+                        ready ^= 1u;
+                    }
                 }
-                mma2_commit_elect(&bar_accum);
+                mma2_commit_elect(&bar_accum[tl % C::kAccs]);
             }
         }
     } else {
@@ -578,7 +748,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
         const uint32_t tmem_d = s_tmem;
         // ------------------------------------------------------------ keep and scale V A
         // this warp's part of the accumulators; n counts these calls
-        auto mask_accumulators = [&](const Tile& t, int n) {
+        auto mask_accumulators = [&](const Tile& t, int tl, int n) {
             grid_dependency_wait();  // the generator's state may be as young as V
             KeepGen gen;
             gen.init(args.drop);
@@ -588,7 +758,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                 for (int ms = 0; ms < t.nsub; ++ms) {
 #pragma unroll 1
                     for (int tt = tbeg; tt < tbeg + kShare && ms * C::kSubT + tt < t.tokens; tt += 32) {
-                        const uint32_t at = tmem_d + lane_base + ms * C::kSubT + tt;
+                        const uint32_t at = tmem_d + lane_base + tl % C::kAccs * C::kAccCols + ms * C::kSubT + tt;
                         uint32_t v[32];
                         tmem_ld_32x32b_x32(at, v);
                         tmem_ld_wait();
@@ -623,7 +793,11 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
 
         // ------------------------------------------------------------ decoders
         const int team = ew / C::kTeamWarps;
-        const int dt = threadIdx.x - 64 - team * C::kTeamThreads;
+        // (into tensor memory a warp writes the lanes of its own quadrant)
+        const int dt = C::kWT ? q * 32 + lane : threadIdx.x - 64 - team * C::kTeamThreads;
+        float level = 0.0f;  // of decode_lane
+#pragma unroll
+        for (int i = 0; i < 16; ++i) level = (lane & 15) == i ? nf4_level(i) : level;
         const bool fp32_scales = args.absmax != nullptr;  // no double quantisation
         const float mu = fp32_scales ? 0.0f : __ldg(args.scale_mean);
         // This thread's unit of a step.  Forward: weight row h0 + dt, block kb.
@@ -642,15 +816,45 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
         const int code_off = DX ? (n_local * kCB + cblk) * 32 : dt * 32;
         // The units' block scales are fetched one own step (several steps of the
         // pair) ahead: an 8-bit code and the second-level scale, or the fp32 scale.
+        // With few tokens and an even number of blocks per row a step's two scales
+        // are one load, and share their second-level scale.
         struct Scale {
             uint32_t ok;  // bit h: the unit lies inside the expert's weight
             int q[C::kKS];
             float a2[C::kKS];
         };
+        constexpr bool kPairs = !DX && C::kKS == 2;
+        const bool pairs = kPairs && args.w_blocks_per_row % 2 == 0 &&
+                           (fp32_scales ? (reinterpret_cast<uintptr_t>(args.absmax) & 7) == 0
+                                        : (reinterpret_cast<uintptr_t>(args.qscale) & 1) == 0);
+        int64_t pair0 = 0;  // of tile t: the first pair, and their number
+        int n_pairs = 0;
+        auto fetch_tile = [&](const Tile& t) {
+            const int row = t.h0 + dt;
+            pair0 = (static_cast<int64_t>(t.g.e) * args.w_rows + row) * (args.w_blocks_per_row / 2) + t.kb0;
+            n_pairs = row < args.w_rows ? min(t.n_main, args.w_blocks_per_row / 2 - t.kb0) : 0;
+        };
         auto fetch = [&](const Tile& t, int it) {
             Scale s;
             s.ok = 0;
             const int k = it - main0(t);
+            if (kPairs && pairs) {
+                const int64_t b = pair0 + k;
+                s.q[0] = 0;
+                s.a2[0] = 0.0f;
+                if (k < n_pairs) {
+                    s.ok = 1;
+                    if (fp32_scales) {
+                        const float2 two = __ldg(reinterpret_cast<const float2*>(args.absmax) + b);
+                        s.a2[0] = two.x;
+                        s.q[0] = __float_as_int(two.y);
+                    } else {
+                        s.q[0] = __ldg(reinterpret_cast<const short*>(args.qscale) + b);
+                        s.a2[0] = __ldg(args.scale2 + (b >> 7));
+                    }
+                }
+                return s;
+            }
             // the first unit's index among the weight's blocks, and the next one's
             const int row0 = DX ? (t.kb0 + k) * C::kKS * 64 + n_local : t.h0 + dt;
             const int blk0 = DX ? t.h0 / 64 + cblk : (t.kb0 + k) * C::kKS;
@@ -678,7 +882,8 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
         // so that a store writes two tokens' 64-byte runs (fp32 partials: 128 bytes
         // of one token).
         auto epilogue = [&](const Tile& t, int tl) {
-            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_accum, tl & 1u, abort_flag) && !*abort_flag);
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_accum[tl % C::kAccs], tl / C::kAccs & 1u, abort_flag) &&
+                                                   !*abort_flag);
             tc_fence_after();
             const uint32_t odd = lane & 1, sel = odd ? 0x3276u : 0x5410u;
             const int col = t.h0 + q * 32 + lane, col2 = col & ~1;
@@ -686,20 +891,23 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
 #pragma unroll 1
                 for (int tt = tbeg; tt < tbeg + kShare && ms * C::kSubT + tt < t.tokens; tt += 32) {
                     uint32_t v[32];
-                    tmem_ld_32x32b_x32(tmem_d + lane_base + ms * C::kSubT + tt, v);
+                    tmem_ld_32x32b_x32(tmem_d + lane_base + tl % C::kAccs * C::kAccCols + ms * C::kSubT + tt, v);
                     tmem_ld_wait();
                     const int at = ms * C::kSubT + tt, left = t.tokens - at;
                     if (args.splits > 1) {
                         float* dst = args.part + (static_cast<int64_t>(t.z) * args.M + t.g.row0 + at) * args.cols + col;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
+                        for (int j = 0; j < 32; ++j) {
+                            if (T <= 64 && j % 8 == 0 && j >= left) break;
                             if (j < left && col < args.cols)
                                 dst[static_cast<int64_t>(j) * args.cols] = __uint_as_float(v[j]);
+                        }
                     } else {
                         uint16_t* dst = args.out + static_cast<int64_t>(t.g.row0 + at + odd) * args.cols + col2;
                         const int rows = col2 < args.cols ? left - static_cast<int>(odd) : 0;  // cols is a multiple of 8
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
+                            if (T <= 64 && j % 8 == 0 && j >= left) break;
                             const uint32_t own = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
                             const uint32_t two = __byte_perm(own, __shfl_xor_sync(0xFFFFFFFFu, own, 1), sel);
                             if (j < rows) *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(j) * args.cols) = two;
@@ -709,65 +917,115 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_pair(lead(&bar_free));
+            if (lane == 0) mbar_arrive_pair(lead(&bar_free[tl % C::kAccs]));
             return ok;
         };
 
         Tile t;
-        bool have = next_tile(0, t), stop = false;
-        int gi = team, it = team;      // this team's next step, and its place in tile t
-        int cs = team, n_masked = 0;   // its code slot; parity of the slot's use in cp
-        uint32_t cp = 0;
+        Walk walk;
+        first_tile(walk);
+        bool have = next_tile(walk, t);
+        // this team's next step: its place in tile t, its slots and the parities of
+        // the rounds over them
+        int it = team, ds = team, cs = team, n_masked = 0;
+        uint32_t cp = 0, dp = 0;
+        bool used = false;  // the decode slot has been used
         Scale ahead{};
-        if (have) ahead = fetch(t, it);
-        for (int tl = 0; have && !stop; ++tl) {
-            const int n_iter = t.n_main + t.n_ext;
-            bool masked = !DROP || t.n_ext == 0;
+        if (have) {
+            if (kPairs) fetch_tile(t);
+            ahead = fetch(t, it);
+        }
+        // A tile's results go out once this team has its first steps of the next
+        // tile in place, so that the MMAs never wait for a decode there.
+        constexpr int kDefer = DS / C::kTeams;
+        Tile last;             // the tile whose results are still to go out, if any
+        bool pending = false, masked = !DROP || t.n_ext == 0;
+        int tl = 0, own = 0;   // own: this team's steps of tile t so far
 #pragma unroll 1
-            for (; it < n_iter; it += C::kTeams, gi += C::kTeams) {
-                const Scale now = ahead;
-                ahead = fetch(t, it + C::kTeams);
-                const bool main_step = is_main(t, it);
-                if (DROP && !masked && main_step) {
-                    masked = true;
-                    mask_accumulators(t, n_masked++);
+        while (true) {
+            const int n_iter = t.n_main + t.n_ext;
+            const bool ended = !have || it >= n_iter;
+            const bool main_step = !ended && is_main(t, it), mask_now = DROP && !masked && (ended || main_step) && have;
+            if (pending && (ended || own == kDefer || mask_now)) {
+                if (!epilogue(last, tl - 1)) break;
+                pending = false;
+            }
+            if (!have) break;
+            if (mask_now) {
+                masked = true;
+                mask_accumulators(t, tl, n_masked++);
+            }
+            if (ended) {
+                last = t;
+                pending = true;
+                own = 0;
+                it -= n_iter;
+                have = next_tile(walk, t);
+                ++tl;
+                if (have) {
+                    if (kPairs) fetch_tile(t);
+                    ahead = fetch(t, it);
+                    masked = !DROP || t.n_ext == 0;
                 }
-                float sc[C::kKS];
+                continue;
+            }
+            float sc[C::kKS];
+            if (kPairs && pairs) {
+                if (fp32_scales) {
+                    sc[0] = ahead.a2[0];
+                    sc[C::kKS - 1] = __int_as_float(ahead.q[0]);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < C::kKS; ++h)
+                        sc[h] = ahead.ok ? nf4_block_scale(static_cast<int8_t>(ahead.q[0] >> 8 * h), ahead.a2[0], mu)
+                                         : 0.0f;
+                }
+            } else {
 #pragma unroll
                 for (int h = 0; h < C::kKS; ++h)
-                    sc[h] = !(now.ok >> h & 1u) ? 0.0f
-                            : fp32_scales       ? now.a2[h]
-                                                : nf4_block_scale(static_cast<int8_t>(now.q[h]), now.a2[h], mu);
-                const bool ok =
-                    mbar_wait(&bar_codes[cs], cp, abort_flag) &&
-                    (!main_step || gi < DS || mbar_wait(&bar_done[gi % DS], ((gi / DS) & 1u) ^ 1u, abort_flag));
-                stop = __any_sync(0xFFFFFFFFu, !ok);  // the warp stays together
-                if (stop) break;
-                if (main_step) {
-#pragma unroll
-                    for (int h = 0; h < C::kKS; ++h) {
-                        uint8_t* dst = w_buf(gi) + h * C::kW + dst_off;
-                        // outside the weight: a zero scale decodes to zeros
-                        decode_row(codes_buf(cs) + h * C::kCodes + code_off, sc[h], dst);
-                    }
-                }
-                // also on an extension step, whose factor tile the copies brought:
-                // the arrival passes on that it has landed
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(lead(&bar_ready[gi % DS]));
-                cs += C::kTeams;
-                if (cs >= LC) {
-                    cs -= LC;
-                    cp ^= 1u;
-                }
+                    sc[h] = !(ahead.ok >> h & 1u) ? 0.0f
+                            : fp32_scales         ? ahead.a2[h]
+                                                  : nf4_block_scale(static_cast<int8_t>(ahead.q[h]), ahead.a2[h], mu);
             }
-            if (DROP && !masked) mask_accumulators(t, n_masked++);
-            const Tile done = t;
-            it -= n_iter;
-            have = !stop && next_tile(tl + 1, t);
-            if (have) ahead = fetch(t, it);
-            if (!epilogue(done, tl)) stop = true;
+            // two polls whose latencies overlap; bounded waits where one is early
+            const bool both = mbar_try_wait(&bar_codes[cs], cp) &
+                              (!main_step || !used || mbar_try_wait(&bar_done[ds], dp ^ 1u));
+            const bool ok = both || (mbar_wait(&bar_codes[cs], cp, abort_flag) &&
+                                     (!main_step || !used || mbar_wait(&bar_done[ds], dp ^ 1u, abort_flag)));
+            if (__any_sync(0xFFFFFFFFu, !ok)) break;  // the warp stays together
+            ahead = fetch(t, it + C::kTeams);
+            // a unit outside the weight has a zero scale and decodes to zeros
+            if (C::kWT && main_step) {
+                tc_fence_after();
+#pragma unroll
+                for (int h = 0; h < C::kKS; ++h)
+                    decode_lane(codes_buf(cs) + h * C::kCodes + code_off, sc[h], level,
+                                tmem_d + lane_base + C::kAccs * C::kAccCols + (ds * C::kKS + h) * 32);
+                tmem_st_wait();
+                tc_fence_before();
+            } else if (main_step) {
+#pragma unroll
+                for (int h = 0; h < C::kKS; ++h)
+                    decode_row(codes_buf(cs) + h * C::kCodes + code_off, sc[h], w_buf(ds) + h * C::kW + dst_off);
+            }
+            // also on an extension step, whose factor tile the copies brought: the
+            // arrival passes on that it has landed
+            if (!C::kWT || !main_step) fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(lead(&bar_ready[ds]));
+            it += C::kTeams;
+            ++own;
+            cs += C::kTeams;
+            if (cs >= LC) {
+                cs -= LC;
+                cp ^= 1u;
+            }
+            ds += C::kTeams;
+            if (ds >= DS) {
+                ds -= DS;
+                dp ^= 1u;
+                used = true;
+            }
         }
     }
     // neither CTA frees its tensor memory or leaves while the other may still

@@ -33,6 +33,7 @@
 
 #include <cstdint>
 
+#include "adapter.h"
 #include "gemm.cuh"
 #include "grouped.cuh"
 #include "philox.cuh"
@@ -61,7 +62,28 @@ struct RankArgs {
     int64_t part_slice;
     uint16_t* out;     // dB [E][N][r] / dA [E][r][K]
     int accumulate;
+    uint16_t* pair;    // T, V in one split: the pair [M, 2 r64] and (or NULL) fp32 [M, r], else partials
+    float* out32;
 };
+
+// v[0 .. 7] = columns j .. j + 7 of a row of T or V: the 16-bit pair, zero beyond
+// r, and the fp32 value.
+__device__ __forceinline__ void store_pair(float (&v)[8], int64_t row, int j, int r, int r64, uint16_t* pair,
+                                           float* out32) {
+    float hi[8], lo[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        if (j + u >= r) v[u] = 0.0f;
+        hi[u] = __bfloat162float(__float2bfloat16_rn(v[u]));
+        lo[u] = v[u] - hi[u];
+        if (out32 != nullptr && j + u < r) out32[row * r + j + u] = v[u];
+    }
+    uint16_t* dst = pair + row * 2 * r64 + j;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3]),
+                                                pack_bf16x2(hi[4], hi[5]), pack_bf16x2(hi[6], hi[7]));
+    *reinterpret_cast<uint4*>(dst + r64) = make_uint4(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]),
+                                                      pack_bf16x2(lo[4], lo[5]), pack_bf16x2(lo[6], lo[7]));
+}
 
 constexpr int kRankStages = 8;  // at most
 template <int MODE, bool DROP>
@@ -178,6 +200,15 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
         n_steps = max(0, min(per, total - step0));
     }
     n_steps = __shfl_sync(0xFFFFFFFFu, n_steps, 0);  // said to be uniform, as what follows from it
+    if (!TOK && args.offsets != nullptr && blockIdx.x == 0 && blockIdx.z == 0) {
+        // offsets that break the contract are reported in the device status word
+        bool bad = false;
+        for (int e = threadIdx.x; e <= args.E; e += C::kThreads) {
+            const int v = __ldcg(args.offsets + e);
+            bad |= v < (e > 0 ? max(0, __ldcg(args.offsets + e - 1)) : 0) || v > args.M;
+        }
+        if (bad) atomicCAS(&g_device_status, 0, kStatusOffsets);
+    }
     const int LS = args.stages, slot_bytes = args.a_bytes + args.b_bytes;
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -385,7 +416,8 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
         if (ok && ew < 8) {
             // T, V: the two halves of the warps share the columns; dB, dA: they
             // take one accumulator each
-            const int cols = TOK ? args.rn : args.rn / 2;
+            const bool pairs = !TOK && args.pair != nullptr;
+            const int cols = TOK ? args.rn : (pairs ? args.r64 : args.rn) / 2;
             const int cbeg = TOK ? 0 : half * cols;
             const int lrow = q * 32 + lane + (TOK ? half * 128 : 0);
             const int row = TOK ? out0 + lrow : g.row0 + lrow;
@@ -394,15 +426,20 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
             const bool direct = part.parts == 1;
             for (int cc = cbeg; cc < cbeg + cols; cc += 8) {
                 uint32_t v[8];
-                if (n_steps > 0) {
+                if (n_steps > 0 && cc < args.rn) {
                     tmem_ld_32x32b_x8(at + cc, v);
                     tmem_ld_wait();
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = 0u;  // a group without rows
+                    for (int j = 0; j < 8; ++j) v[j] = 0u;  // a group without rows; columns beyond r
                 }
                 if (!row_ok) continue;
-                if constexpr (!TOK) {
+                if (pairs) {
+                    float x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(v[j]) * args.alpha;
+                    store_pair(x, row, cc, args.r, args.r64, args.pair, args.out32);
+                } else if constexpr (!TOK) {
                     float* dst = args.part + blockIdx.z * args.part_slice + static_cast<int64_t>(row) * args.rn + cc;
                     *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
                     *reinterpret_cast<uint4*>(dst + 4) = make_uint4(v[4], v[5], v[6], v[7]);
@@ -473,7 +510,6 @@ struct RankRowsSumArgs {
     float alpha;
     uint16_t* pair;
     float* out32;  // or NULL
-    int check;     // 1: report offsets that break the contract in the device status word
 };
 
 __global__ void k_rank_rows_sum(const RankRowsSumArgs a) {
@@ -483,43 +519,34 @@ __global__ void k_rank_rows_sum(const RankRowsSumArgs a) {
     if (a.offsets != nullptr) {
         lo = min(max(__ldcg(a.offsets), 0), a.M);
         hi = min(max(__ldcg(a.offsets + a.E), lo), a.M);
-        if (a.check && blockIdx.x == 0) {
-            bool bad = false;
-            for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
-                const int v = __ldcg(a.offsets + e);
-                bad |= v < (e > 0 ? max(0, __ldcg(a.offsets + e - 1)) : 0) || v > a.M;
-            }
-            if (bad) atomicCAS(&g_device_status, 0, kStatusOffsets);
-        }
     }
-    const int quads = a.r64 / 4;
-    const int64_t total = static_cast<int64_t>(hi - lo) * quads;
+    const int octs = a.r64 / 8;
+    const int64_t total = static_cast<int64_t>(hi - lo) * octs;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t row = lo + i / quads;
-        const int j = 4 * static_cast<int>(i % quads);
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const int64_t row = lo + i / octs;
+        const int j = 8 * static_cast<int>(i % octs);
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = 0.0f;
         if (j < a.rn) {
             const float* p = a.part + row * a.rn + j;
-            for (int z = 0; z < a.splits; ++z) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(p + z * a.slice));
+            for (int z = 0; z < a.splits; ++z, p += a.slice) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(p) + 1);
                 v[0] += x.x;
                 v[1] += x.y;
                 v[2] += x.z;
                 v[3] += x.w;
+                v[4] += y.x;
+                v[5] += y.y;
+                v[6] += y.z;
+                v[7] += y.w;
             }
         }
-        float hi4[4], lo4[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            v[u] = j + u < a.r ? v[u] * a.alpha : 0.0f;
-            hi4[u] = __bfloat162float(__float2bfloat16_rn(v[u]));
-            lo4[u] = v[u] - hi4[u];
-            if (a.out32 != nullptr && j + u < a.r) a.out32[row * a.r + j + u] = v[u];
-        }
-        uint16_t* dst = a.pair + row * 2 * a.r64 + j;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(hi4[0], hi4[1]), pack_bf16x2(hi4[2], hi4[3]));
-        *reinterpret_cast<uint2*>(dst + a.r64) = make_uint2(pack_bf16x2(lo4[0], lo4[1]), pack_bf16x2(lo4[2], lo4[3]));
+        for (int u = 0; u < 8; ++u) v[u] *= a.alpha;
+        store_pair(v, row, j, a.r, a.r64, a.pair, a.out32);
     }
 }
 
@@ -527,15 +554,16 @@ __global__ void k_rank_rows_sum(const RankRowsSumArgs a) {
 __global__ void k_rank_pair(const float* __restrict__ src, int64_t M, int r, int r64, uint16_t* __restrict__ pair) {
     grid_dependency_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t total = M * r64;
+    const int octs = r64 / 8;
+    const int64_t total = M * octs;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t m = i / r64;
-        const int j = static_cast<int>(i % r64);
-        const float v = j < r ? src[m * r + j] : 0.0f;
-        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-        pair[m * 2 * r64 + j] = *reinterpret_cast<const uint16_t*>(&hi);
-        pair[m * 2 * r64 + r64 + j] = bf16_bits(v - __bfloat162float(hi));
+        const int64_t row = i / octs;
+        const int j = 8 * static_cast<int>(i % octs);
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = j + u < r ? __ldcg(src + row * r + j + u) : 0.0f;
+        store_pair(v, row, j, r, r64, pair, nullptr);
     }
 }
 
