@@ -180,7 +180,7 @@ int64_t most_partials(int E, int64_t M, int part_steps) {
 // a split contraction the partials' way through memory and one more kernel).
 // The groups are taken as equal, which the host has to.
 struct FusedPlan {
-    bool few;       // 32-token tiles, two CTAs per SM; else up to 512 tokens, one CTA
+    int tile;       // the kernel: tiles of up to 32 (two CTAs per SM), 256 or 512 tokens
     int tile_rows;
     int splits;
     int k_main, k_ext;  // steps
@@ -189,27 +189,24 @@ struct FusedPlan {
 FusedPlan plan_fused(int E, int64_t M, int64_t cols, int64_t contraction, int r, int num_sms) {
     const int64_t groups = std::min<int64_t>(E, M), mean = div_up(M, groups), col_tiles = div_up(cols, 256);
     FusedPlan best{};
-    best.few = mean <= 24;
-    const int wide = best.few ? 128 : 64;
-    best.k_main = static_cast<int>(div_up(contraction, wide));
-    best.k_ext = 2 * rank64(r) / wide;
+    const bool few = mean <= 24;
     double best_cost = 1e30;
-    const int64_t pairs = num_sms / 2 * (best.few ? 2 : 1);
-    for (int rows = best.few ? 32 : 512; rows >= 32; rows -= 32) {
+    const int64_t pairs = num_sms / 2 * (few ? 2 : 1);
+    for (int rows = few ? 32 : 512; rows >= 32; rows -= 32) {
         const int64_t per_group = div_up(mean, rows), size = ceil_to(div_up(mean, per_group), 32);
         const int64_t tiles = groups * per_group * col_tiles;
+        const int tile = few ? 32 : rows <= 256 ? 256 : 512, wide = tile == 512 ? 64 : 128;
+        const int k_main = static_cast<int>(div_up(contraction, wide)), k_ext = 2 * rank64(r) / wide;
+        const double step = few ? 1500.0 : tile == 256 ? std::max(4.2 * size + 100.0, 1200.0) : std::max(2.2 * size, 1050.0);
         // many tokens: only to put work on every SM at all
-        const int most = best.few ? 8 : static_cast<int>(std::min<int64_t>(8, pairs / tiles));
-        for (int splits = 1; splits <= std::max(1, most) && (splits == 1 || splits * 4 <= best.k_main); ++splits) {
+        const int most = few ? 8 : static_cast<int>(std::min<int64_t>(8, pairs / tiles));
+        for (int splits = 1; splits <= std::max(1, most) && (splits == 1 || splits * 4 <= k_main); ++splits) {
             const double rounds = static_cast<double>(div_up(tiles * splits, pairs));
-            const double step = best.few ? 1500.0 : std::max(2.1 * size + 250.0, 500.0);
-            double cost = rounds * (step * static_cast<double>(div_up(best.k_main, splits) + best.k_ext) + 3000.0 +
-                                    16.0 * size);
+            double cost = rounds * (step * static_cast<double>(div_up(k_main, splits) + k_ext) + 3000.0 + 16.0 * size);
             if (splits > 1) cost += 6000.0 + static_cast<double>(splits) * M * cols * 8 / 2000.0;
             if (cost < 0.97 * best_cost) {
                 best_cost = cost;
-                best.tile_rows = rows;
-                best.splits = splits;
+                best = {tile, rows, splits, k_main, k_ext};
             }
         }
     }
@@ -471,7 +468,9 @@ int fused(const GroupCtx& c, bool dx, const uint16_t* act, const uint16_t* pair,
                       : launch_group_gemm<true, T, false>("group_gemm_dx", f, g, cols_fastest, c.num_sms, &mapped,
                                                           c.stream);
     };
-    cudaError_t e = plan.few ? go(std::integral_constant<int, 32>()) : go(std::integral_constant<int, 512>());
+    cudaError_t e = plan.tile == 32    ? go(std::integral_constant<int, 32>())
+                    : plan.tile == 256 ? go(std::integral_constant<int, 256>())
+                                       : go(std::integral_constant<int, 512>());
     if (e != cudaSuccess) return -2;
     if (!mapped) return -1;
     if (plan.splits > 1) {

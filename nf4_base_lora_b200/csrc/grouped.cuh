@@ -237,6 +237,15 @@ __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorM
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map, uint32_t cluster_bar,
+                                                 int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
 // Arrive on a barrier of either CTA of the pair (a shared::cluster address).
 // The default form, at CTA scope: what it publishes are operand tiles that only
 // MMAs read, ordered for them by the proxy fence before it, and accumulators,
@@ -360,29 +369,35 @@ struct GroupGemmConfig {
     static constexpr int kSubs = T > 256 ? 2 : 1;      // accumulators
     static constexpr int kSubT = T / kSubs;            // tokens of one, half of them per CTA
     static constexpr bool kWT = T <= 64 && !DX;
-    static constexpr int kTeams = T > 64 ? 4 : 2;
-    static constexpr int kKS = T > 64 ? 1 : 2;  // 64s of the contraction in a step
-    static constexpr int kDS = T > 64 ? 4 : kWT ? 3 : 2;  // slots of decoded tiles and of tokens
-    static constexpr int kLC = 2 * kDS;                // slots of packed codes
+    static constexpr int kTeams = T > 256 ? 4 : 2;
+    static constexpr int kKS = T > 256 ? 1 : 2;        // 64s of the contraction in a step
+    static constexpr int kUnits = T > 64 ? 1 : 2;      // (row, block) units of a step per thread
+    static constexpr int kDS = T > 256 ? 4 : T > 64 || kWT ? 3 : 2;  // slots of decoded tiles and of tokens
+    static constexpr int kLC = T > 256 ? 8 : T > 64 ? 4 : 2 * kDS;   // slots of packed codes
     static constexpr int kWS = kWT ? 1 : kDS;          // slots of weight tiles in shared memory (kWT: extension only)
     static constexpr int kSub = kSubT / 2 * 128;       // a CTA's tokens of one accumulator, 64 deep
     static constexpr int kTok = kSubs * kSub;          // of all accumulators
     static constexpr int kCodes = kBM * 32, kW = kBM * 128;  // a packed and a decoded tile, 64 deep
     static constexpr int kTokBytes = kKS * kTok, kCBytes = kKS * kCodes, kWBytes = kKS * kW;
     static constexpr int kSmem = kDS * kTokBytes + kWS * kWBytes + kLC * kCBytes + 1024;
-    static constexpr int kTeamThreads = kBM;           // one (row, block) unit each
+    static constexpr int kTeamThreads = kBM * (kKS / kUnits);
     static constexpr int kTeamWarps = kTeamThreads / 32;
     static constexpr int kWorkWarps = kTeamWarps * kTeams;
-    static constexpr int kThreads = 64 + 32 * kWorkWarps;
+    // With one CTA per SM a warp of its own copies the codes, into slots that the
+    // decoders free (else the copying warp's turns, some 600 clocks a step, bound
+    // all tiles of few tokens); with two the registers do not go round for it.
+    static constexpr bool kCodeWarp = T > 64;
+    static constexpr int kThreads = 64 + 32 * kWorkWarps + (kCodeWarp ? 32 : 0);
     static constexpr int kMinBlocks = T > 64 ? 1 : 2;
-    static constexpr int kAccs = T > 64 || kWT ? 1 : 2;       // accumulator sets: the next tile's MMAs run beside the epilogue
+    static constexpr int kAccs = T > 256 || kWT ? 1 : 2;       // accumulator sets: the next tile's MMAs run beside the epilogue
     static constexpr int kAccCols = T;                 // columns of a set
     static constexpr int kTmemCols = kWT ? 256 : kAccs * T;
     static constexpr uint32_t kIdesc = make_idesc_bf16(2 * kBM, 0, DX ? 1 : 0, 0);  // without N
     // A wait for a barrier's phase is sound only where the phase before it is
-    // known to be complete: a slot is always the same team's, or (three slots) that
-    // phase belongs to a step whose successor this team has seen multiplied.
-    static_assert((kDS % kTeams == 0 || kDS == kTeams + 1) && kLC % kTeams == 0 && kLC >= kDS, "rings");
+    // known to be complete.  Code slots: a slot is always the same team's.  Decode
+    // slots: that phase is of the step 2 kDS before, not after the one whose MMAs
+    // (they complete in order) the team has waited for at its last step.
+    static_assert(kDS >= kTeams && kLC % kTeams == 0 && kLC >= kDS, "rings");
     static_assert(!kWT || kAccs * T + kDS * kKS * 32 <= kTmemCols, "tensor memory");
     static_assert(kSub % 1024 == 0 && kSmem * kMinBlocks <= 226 * 1024, "shared memory");
 };
@@ -403,8 +418,8 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
     extern __shared__ __align__(16) uint8_t smem_raw[];
     // bar_ready, bar_masked and bar_free count both CTAs, in the leading one
     // (rank 0); the MMAs' completions (bar_done, bar_accum, bar_ext) arrive in
-    // both; bar_codes is each CTA's own
-    __shared__ uint64_t bar_codes[LC], bar_ready[DS], bar_done[DS], bar_accum[C::kAccs], bar_ext, bar_masked,
+    // both; bar_codes and bar_cfree are each CTA's own
+    __shared__ uint64_t bar_codes[LC], bar_cfree[LC], bar_ready[DS], bar_done[DS], bar_accum[C::kAccs], bar_ext, bar_masked,
         bar_free[C::kAccs];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
@@ -502,7 +517,10 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
     auto codes_buf = [&](int cs) { return base + DS * C::kTokBytes + C::kWS * C::kWBytes + cs * C::kCBytes; };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < LC; ++i) mbar_init(&bar_codes[i], 1);
+        for (int i = 0; i < LC; ++i) {
+            mbar_init(&bar_codes[i], 1);
+            mbar_init(&bar_cfree[i], C::kTeamWarps);
+        }
         for (int i = 0; i < DS; ++i) {
             mbar_init(&bar_ready[i], 1 + 2 * C::kTeamWarps);
             mbar_init(&bar_done[i], 1);
@@ -544,6 +562,28 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
     // the leading CTA's copy of a barrier (shared::cluster address)
     auto lead = [&](uint64_t* bar) { return cluster_map(smem_u32(bar), 0); };
 
+    // packed codes of step it into slot cs; an extension step, whose factor tile
+    // goes with its tokens, completes the slot's phase without any.  The whole warp
+    // calls it.
+    auto load_codes = [&](const Tile& t, int it, int cs) {
+        if (elect_one()) {
+            uint64_t* bar = &bar_codes[cs];
+            if (is_main(t, it)) {
+                mbar_arrive_expect_tx(bar, C::kCBytes);
+                const int kb = (t.kb0 + it - main0(t)) * C::kKS;
+#pragma unroll
+                for (int h = 0; h < C::kKS; ++h) {
+                    uint8_t* dst = codes_buf(cs) + h * C::kCodes;
+                    if constexpr (DX) tma_load_3d(dst, &map_w, bar, t.h0 / 2, (kb + h) * 64, t.g.e);
+                    else tma_load_3d(dst, &map_w, bar, (kb + h) * 32, t.h0, t.g.e);
+                }
+            } else {
+                mbar_arrive(bar);
+            }
+        }
+        __syncwarp();
+    };
+
     if (warp == 0) {
         // ------------------------------------------------------------ copies
         if (lane == 0) {
@@ -554,30 +594,18 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
         }
         __syncwarp();
         bool waited = false;
-        // the codes run kAhead steps before the tokens, into the next tile
-        constexpr int kAhead = LC - DS;
+        // without a warp of their own the codes run kAhead steps before the tokens,
+        // into the next tile
+        constexpr int kAhead = C::kCodeWarp ? 0 : LC - DS;
         Tile tc, tt;  // tiles of the codes' and of the tokens' step
         Walk wc, wt;
         first_tile(wc);
         wt = wc;
         int itc = 0, csc = 0;
-        bool have_c = next_tile(wc, tc);
-        // packed codes of step itc, or nothing on an extension step, whose factor
-        // tile goes with its tokens
+        bool have_c = !C::kCodeWarp && next_tile(wc, tc);
         auto codes_step = [&]() {
-            if (!have_c) return;
-            if (is_main(tc, itc) && elect_one()) {
-                uint64_t* bar = &bar_codes[csc];
-                mbar_arrive_expect_tx(bar, C::kCBytes);
-                const int kb = (tc.kb0 + itc - main0(tc)) * C::kKS;
-#pragma unroll
-                for (int h = 0; h < C::kKS; ++h) {
-                    uint8_t* dst = codes_buf(csc) + h * C::kCodes;
-                    if constexpr (DX) tma_load_3d(dst, &map_w, bar, tc.h0 / 2, (kb + h) * 64, tc.g.e);
-                    else tma_load_3d(dst, &map_w, bar, (kb + h) * 32, tc.h0, tc.g.e);
-                }
-            }
-            __syncwarp();
+            if (C::kCodeWarp || !have_c) return;
+            load_codes(tc, itc, csc);
             if (++csc == LC) csc = 0;
             if (++itc == tc.n_main + tc.n_ext) {
                 itc = 0;
@@ -585,9 +613,8 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             }
         };
         for (int i = 0; i < kAhead; ++i) codes_step();
-        int ds = 0, cs = 0;     // slots of the tokens' step
+        int ds = 0;             // slot of the tokens' step
         uint32_t done = 0;      // parity of the round over the slots
-        bool used = false;      // every slot has been used
         bool stop = false;
         while (!stop && next_tile(wt, tt)) {
             const int n_iter = tt.n_main + tt.n_ext;
@@ -595,7 +622,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                 // the step DS before is multiplied: its token and decode slots are
                 // free, and so is the code slot of the step kAhead ahead, which its
                 // decode has read.  The warp stays together also when a wait gives up.
-                stop = __any_sync(0xFFFFFFFFu, (used && !mbar_wait(&bar_done[ds], done ^ 1u, abort_flag)) || *abort_flag);
+                stop = __any_sync(0xFFFFFFFFu, !mbar_wait(&bar_done[ds], done ^ 1u, abort_flag) || *abort_flag);
                 if (stop) break;
                 const bool main_step = is_main(tt, it);
                 const int j0 = (DROP ? it : it - tt.n_main) * C::kKS;  // of an extension step
@@ -607,7 +634,8 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                     if (stop) break;
                 }
                 if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(&bar_ready[ds], 2 * C::kKS * tt.nsub * C::kSub);
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(&bar_ready[ds], 2 * (C::kKS * tt.nsub * C::kSub + (main_step ? 0 : C::kWBytes)));
                     const uint32_t bar = lead(&bar_ready[ds]);
                     if (main_step) {
                         const int kb = (tt.kb0 + it - main0(tt)) * C::kKS;
@@ -621,8 +649,6 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                         const int half = tt.n_ext * C::kKS / 2;
                         if (!waited) grid_dependency_wait();
                         waited = true;
-                        uint64_t* wbar = &bar_codes[cs];
-                        mbar_arrive_expect_tx(wbar, C::kWBytes);
 #pragma unroll
                         for (int h = 0; h < C::kKS; ++h) {
                             const int j = j0 + h, jb = j % half;
@@ -633,19 +659,17 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                             if constexpr (DX) {
 #pragma unroll
                                 for (int c = 0; c < C::kBM / 64; ++c)
-                                    tma_load_3d(dst + c * 8192, &map_we, wbar, tt.h0 + c * 64, jb * 64, tt.g.e);
+                                    tma_load_3d_pair(dst + c * 8192, &map_we, bar, tt.h0 + c * 64, jb * 64, tt.g.e);
                             } else {
-                                tma_load_3d(dst, &map_we, wbar, jb * 64, tt.h0, tt.g.e);
+                                tma_load_3d_pair(dst, &map_we, bar, jb * 64, tt.h0, tt.g.e);
                             }
                         }
                     }
                 }
                 __syncwarp();
-                if (++cs == LC) cs = 0;
                 if (++ds == DS) {
                     ds = 0;
                     done ^= 1u;
-                    used = true;
                 }
                 codes_step();
             }
@@ -733,6 +757,30 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                 mma2_commit_elect(&bar_accum[tl % C::kAccs]);
             }
         }
+    } else if (C::kCodeWarp && warp == 2 + C::kWorkWarps) {
+        // ------------------------------------------------------------ codes
+        Tile t;
+        Walk walk;
+        first_tile(walk);
+        int cs = 0;
+        uint32_t freed = 0;
+        bool stop = false;
+        while (!stop && next_tile(walk, t)) {
+            const int n_iter = t.n_main + t.n_ext;
+            for (int it = 0; it < n_iter; ++it) {
+                stop = __any_sync(0xFFFFFFFFu, !mbar_wait(&bar_cfree[cs], freed ^ 1u, abort_flag) || *abort_flag);
+                if (stop) break;
+                load_codes(t, it, cs);
+                if (++cs == LC) {
+                    cs = 0;
+                    freed ^= 1u;
+                }
+            }
+        }
+        if (stop) {  // as above
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 1000000) {}
+        }
     } else {
         const int ew = warp - 2;
         const int q = warp & 3;  // tensor memory lane quadrant of this warp
@@ -793,8 +841,10 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
 
         // ------------------------------------------------------------ decoders
         const int team = ew / C::kTeamWarps;
+        // a thread of kBM; with as many threads as a step has units, which 64 of it
         // (into tensor memory a warp writes the lanes of its own quadrant)
-        const int dt = C::kWT ? q * 32 + lane : threadIdx.x - 64 - team * C::kTeamThreads;
+        const int dt = C::kWT ? q * 32 + lane : (threadIdx.x - 64) % C::kBM;
+        const int half = C::kKS > C::kUnits ? (threadIdx.x - 64) / C::kBM % (C::kKS / C::kUnits) : 0;
         float level = 0.0f;  // of decode_lane
 #pragma unroll
         for (int i = 0; i < 16; ++i) level = (lane & 15) == i ? nf4_level(i) : level;
@@ -812,60 +862,62 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             n_local = 8 * (qw >> 1) + i;
             cblk = ((i >> 1) + qw) & 1;
         }
-        const int dst_off = DX ? cblk * 8192 + n_local * 128 + ((n_local & 7) << 4) : dt * 128 + ((dt & 7) << 4);
-        const int code_off = DX ? (n_local * kCB + cblk) * 32 : dt * 32;
+        const int dst_off = half * C::kW + (DX ? cblk * 8192 + n_local * 128 + ((n_local & 7) << 4) : dt * 128 + ((dt & 7) << 4));
+        const int code_off = half * C::kCodes + (DX ? n_local * kCB + cblk : dt) * 32;
         // The units' block scales are fetched one own step (several steps of the
         // pair) ahead: an 8-bit code and the second-level scale, or the fp32 scale.
         // With few tokens and an even number of blocks per row a step's two scales
-        // are one load, and share their second-level scale.
+        // are one load, and share their second-level scale.  Every instruction here
+        // is one that the decode's pipe has no time for, so that what depends on the
+        // tile alone is worked out once for it (indices of blocks fit 32 bits).
         struct Scale {
             uint32_t ok;  // bit h: the unit lies inside the expert's weight
-            int q[C::kKS];
-            float a2[C::kKS];
+            int q[C::kUnits];
+            float a2[C::kUnits];
         };
-        constexpr bool kPairs = !DX && C::kKS == 2;
+        constexpr bool kPairs = !DX && C::kUnits == 2;
         const bool pairs = kPairs && args.w_blocks_per_row % 2 == 0 &&
                            (fp32_scales ? (reinterpret_cast<uintptr_t>(args.absmax) & 7) == 0
                                         : (reinterpret_cast<uintptr_t>(args.qscale) & 1) == 0);
-        int64_t pair0 = 0;  // of tile t: the first pair, and their number
-        int n_pairs = 0;
-        auto fetch_tile = [&](const Tile& t) {
-            const int row = t.h0 + dt;
-            pair0 = (static_cast<int64_t>(t.g.e) * args.w_rows + row) * (args.w_blocks_per_row / 2) + t.kb0;
-            n_pairs = row < args.w_rows ? min(t.n_main, args.w_blocks_per_row / 2 - t.kb0) : 0;
+        const uint32_t k_blocks = DX ? C::kKS * 64 * static_cast<uint32_t>(args.w_blocks_per_row) : C::kKS;
+        uint32_t block0 = 0;       // of the first unit in step 0 of tile t's contraction
+        int k_end[C::kUnits] = {}; // unit h exists in the steps before this one
+        auto enter = [&](const Tile& t) {
+            const int kb = t.kb0 * C::kKS + half;
+            const int row = DX ? kb * 64 + n_local : t.h0 + dt, blk = DX ? t.h0 / 64 + cblk : kb;
+            block0 = (static_cast<uint32_t>(t.g.e) * args.w_rows + row) * args.w_blocks_per_row + blk;
+            const bool inside = DX ? blk < args.w_blocks_per_row : row < args.w_rows;
+            const int kbs = DX ? (args.w_rows - n_local + 63) >> 6 : args.w_blocks_per_row;  // 64s of the thread's units
+#pragma unroll
+            for (int h = 0; h < C::kUnits; ++h)
+                k_end[h] = inside ? min(t.n_main, (kbs - half - h + C::kKS - 1) / C::kKS - t.kb0) : 0;
         };
-        auto fetch = [&](const Tile& t, int it) {
+        auto fetch = [&](int k) {
             Scale s;
             s.ok = 0;
-            const int k = it - main0(t);
+            const uint32_t b0 = block0 + static_cast<uint32_t>(k) * k_blocks;
             if (kPairs && pairs) {
-                const int64_t b = pair0 + k;
                 s.q[0] = 0;
                 s.a2[0] = 0.0f;
-                if (k < n_pairs) {
+                if (k < k_end[0]) {
                     s.ok = 1;
                     if (fp32_scales) {
-                        const float2 two = __ldg(reinterpret_cast<const float2*>(args.absmax) + b);
+                        const float2 two = __ldg(reinterpret_cast<const float2*>(args.absmax + b0));
                         s.a2[0] = two.x;
                         s.q[0] = __float_as_int(two.y);
                     } else {
-                        s.q[0] = __ldg(reinterpret_cast<const short*>(args.qscale) + b);
-                        s.a2[0] = __ldg(args.scale2 + (b >> 7));
+                        s.q[0] = __ldg(reinterpret_cast<const short*>(args.qscale + b0));
+                        s.a2[0] = __ldg(args.scale2 + (b0 >> 8));
                     }
                 }
                 return s;
             }
-            // the first unit's index among the weight's blocks, and the next one's
-            const int row0 = DX ? (t.kb0 + k) * C::kKS * 64 + n_local : t.h0 + dt;
-            const int blk0 = DX ? t.h0 / 64 + cblk : (t.kb0 + k) * C::kKS;
-            const int64_t b0 = (static_cast<int64_t>(t.g.e) * args.w_rows + row0) * args.w_blocks_per_row + blk0;
 #pragma unroll
-            for (int h = 0; h < C::kKS; ++h) {
+            for (int h = 0; h < C::kUnits; ++h) {
                 s.q[h] = 0;
                 s.a2[h] = 0.0f;
-                const int64_t b = b0 + (DX ? static_cast<int64_t>(h) * 64 * args.w_blocks_per_row : h);
-                if (k >= 0 && k < t.n_main && row0 + (DX ? 64 * h : 0) < args.w_rows &&
-                    blk0 + (DX ? 0 : h) < args.w_blocks_per_row) {
+                const uint32_t b = b0 + (DX ? h * 64 * static_cast<uint32_t>(args.w_blocks_per_row) : h);
+                if ((!DROP || k >= 0) && k < k_end[h]) {
                     s.ok |= 1u << h;
                     if (fp32_scales) {
                         s.a2[h] = __ldg(args.absmax + b);
@@ -928,93 +980,97 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
         // this team's next step: its place in tile t, its slots and the parities of
         // the rounds over them
         int it = team, ds = team, cs = team, n_masked = 0;
-        uint32_t cp = 0, dp = 0;
-        bool used = false;  // the decode slot has been used
+        uint32_t cp = 0, dp = 1;
+        const uint32_t ready0 = lead(&bar_ready[0]);
         Scale ahead{};
         if (have) {
-            if (kPairs) fetch_tile(t);
-            ahead = fetch(t, it);
+            enter(t);
+            ahead = fetch(it - main0(t));
         }
         // A tile's results go out once this team has its first steps of the next
         // tile in place, so that the MMAs never wait for a decode there.
         constexpr int kDefer = DS / C::kTeams;
         Tile last;             // the tile whose results are still to go out, if any
         bool pending = false, masked = !DROP || t.n_ext == 0;
-        int tl = 0, own = 0;   // own: this team's steps of tile t so far
+        int tl = 0, own = -1;  // own: with a tile pending, this team's steps of tile t so far
+        int n_iter = t.n_main + t.n_ext;
 #pragma unroll 1
         while (true) {
-            const int n_iter = t.n_main + t.n_ext;
             const bool ended = !have || it >= n_iter;
-            const bool main_step = !ended && is_main(t, it), mask_now = DROP && !masked && (ended || main_step) && have;
-            if (pending && (ended || own == kDefer || mask_now)) {
-                if (!epilogue(last, tl - 1)) break;
-                pending = false;
-            }
-            if (!have) break;
-            if (mask_now) {
-                masked = true;
-                mask_accumulators(t, tl, n_masked++);
-            }
-            if (ended) {
-                last = t;
-                pending = true;
-                own = 0;
-                it -= n_iter;
-                have = next_tile(walk, t);
-                ++tl;
-                if (have) {
-                    if (kPairs) fetch_tile(t);
-                    ahead = fetch(t, it);
-                    masked = !DROP || t.n_ext == 0;
+            if (ended || own == kDefer || (DROP && !masked)) {
+                const bool mask_now = DROP && !masked && (ended || is_main(t, it)) && have;
+                if (pending && (ended || own == kDefer || mask_now)) {
+                    if (!epilogue(last, tl - 1)) break;
+                    pending = false;
+                    own = -1;
                 }
-                continue;
+                if (!have) break;
+                if (mask_now) {
+                    masked = true;
+                    mask_accumulators(t, tl, n_masked++);
+                }
+                if (ended) {
+                    last = t;
+                    pending = true;
+                    own = 0;
+                    it -= n_iter;
+                    have = next_tile(walk, t);
+                    ++tl;
+                    if (have) {
+                        enter(t);
+                        ahead = fetch(it - main0(t));
+                        masked = !DROP || t.n_ext == 0;
+                        n_iter = t.n_main + t.n_ext;
+                    }
+                    continue;
+                }
             }
-            float sc[C::kKS];
+            const bool main_step = is_main(t, it);
+            float sc[C::kUnits];
             if (kPairs && pairs) {
                 if (fp32_scales) {
                     sc[0] = ahead.a2[0];
-                    sc[C::kKS - 1] = __int_as_float(ahead.q[0]);
+                    sc[C::kUnits - 1] = __int_as_float(ahead.q[0]);
                 } else {
 #pragma unroll
-                    for (int h = 0; h < C::kKS; ++h)
+                    for (int h = 0; h < C::kUnits; ++h)
                         sc[h] = ahead.ok ? nf4_block_scale(static_cast<int8_t>(ahead.q[0] >> 8 * h), ahead.a2[0], mu)
                                          : 0.0f;
                 }
             } else {
 #pragma unroll
-                for (int h = 0; h < C::kKS; ++h)
+                for (int h = 0; h < C::kUnits; ++h)
                     sc[h] = !(ahead.ok >> h & 1u) ? 0.0f
                             : fp32_scales         ? ahead.a2[h]
                                                   : nf4_block_scale(static_cast<int8_t>(ahead.q[h]), ahead.a2[h], mu);
             }
             // two polls whose latencies overlap; bounded waits where one is early
-            const bool both = mbar_try_wait(&bar_codes[cs], cp) &
-                              (!main_step || !used || mbar_try_wait(&bar_done[ds], dp ^ 1u));
-            const bool ok = both || (mbar_wait(&bar_codes[cs], cp, abort_flag) &&
-                                     (!main_step || !used || mbar_wait(&bar_done[ds], dp ^ 1u, abort_flag)));
+            const bool both = mbar_try_wait(&bar_codes[cs], cp) & mbar_try_wait(&bar_done[ds], dp);
+            const bool ok = both || (mbar_wait(&bar_codes[cs], cp, abort_flag) && mbar_wait(&bar_done[ds], dp, abort_flag));
             if (__any_sync(0xFFFFFFFFu, !ok)) break;  // the warp stays together
-            ahead = fetch(t, it + C::kTeams);
+            it += C::kTeams;
+            ahead = fetch(it - main0(t));
             // a unit outside the weight has a zero scale and decodes to zeros
             if (C::kWT && main_step) {
                 tc_fence_after();
 #pragma unroll
-                for (int h = 0; h < C::kKS; ++h)
+                for (int h = 0; h < C::kUnits; ++h)
                     decode_lane(codes_buf(cs) + h * C::kCodes + code_off, sc[h], level,
                                 tmem_d + lane_base + C::kAccs * C::kAccCols + (ds * C::kKS + h) * 32);
                 tmem_st_wait();
                 tc_fence_before();
             } else if (main_step) {
 #pragma unroll
-                for (int h = 0; h < C::kKS; ++h)
+                for (int h = 0; h < C::kUnits; ++h)
                     decode_row(codes_buf(cs) + h * C::kCodes + code_off, sc[h], w_buf(ds) + h * C::kW + dst_off);
             }
-            // also on an extension step, whose factor tile the copies brought: the
-            // arrival passes on that it has landed
-            if (!C::kWT || !main_step) fence_proxy_async_smem();
+            if (!C::kWT) fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_pair(lead(&bar_ready[ds]));
-            it += C::kTeams;
-            ++own;
+            if (lane == 0) {
+                if (C::kCodeWarp) mbar_arrive(&bar_cfree[cs]);
+                mbar_arrive_pair(ready0 + 8 * ds);
+            }
+            if (own >= 0) ++own;
             cs += C::kTeams;
             if (cs >= LC) {
                 cs -= LC;
@@ -1024,7 +1080,6 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             if (ds >= DS) {
                 ds -= DS;
                 dp ^= 1u;
-                used = true;
             }
         }
     }
