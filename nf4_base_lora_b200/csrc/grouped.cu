@@ -175,9 +175,13 @@ int64_t most_partials(int E, int64_t M, int part_steps) {
 }
 
 // How the fused product is cut: by a model of its time in clocks, from the
-// measured parts (per step of a tile 2 clocks a token of MMAs, at least the
-// decode's share; per tile its start, its end and the stores of its results; for
-// a split contraction the partials' way through memory and one more kernel).
+// measured parts (per step of a tile the decode's and the issue's share and a term
+// for its tokens; per tile its start, its end and, where the next tile's MMAs wait
+// for them, the stores of its results; for a split contraction the partials' way
+// through memory and one more kernel).  Measured at the choice between the two
+// kernels for many tokens: 125 tokens in each of 64 experts of 2048 x 1408, a
+// training step: 328 us with 256-token tiles, 345 with 512; 1024 in each of eight
+// of 4096 x 11008: 1570 against 1295.
 // The groups are taken as equal, which the host has to.
 struct FusedPlan {
     int tile;       // the kernel: tiles of up to 32 (two CTAs per SM), 256 or 512 tokens
@@ -197,12 +201,15 @@ FusedPlan plan_fused(int E, int64_t M, int64_t cols, int64_t contraction, int r,
         const int64_t tiles = groups * per_group * col_tiles;
         const int tile = few ? 32 : rows <= 256 ? 256 : 512, wide = tile == 512 ? 64 : 128;
         const int k_main = static_cast<int>(div_up(contraction, wide)), k_ext = 2 * rank64(r) / wide;
-        const double step = few ? 1500.0 : tile == 256 ? std::max(4.2 * size + 100.0, 1200.0) : std::max(2.2 * size, 1050.0);
+        const double step = few           ? 1500.0
+                            : tile == 256 ? 1600.0 + 1.2 * size
+                                         : std::max(700.0 + 0.8 * size, 930.0);
+        const double ends = few || tile == 256 ? 4000.0 : 3000.0 + 16.0 * size;
         // many tokens: only to put work on every SM at all
         const int most = few ? 8 : static_cast<int>(std::min<int64_t>(8, pairs / tiles));
         for (int splits = 1; splits <= std::max(1, most) && (splits == 1 || splits * 4 <= k_main); ++splits) {
             const double rounds = static_cast<double>(div_up(tiles * splits, pairs));
-            double cost = rounds * (step * static_cast<double>(div_up(k_main, splits) + k_ext) + 3000.0 + 16.0 * size);
+            double cost = rounds * (step * static_cast<double>(div_up(k_main, splits) + k_ext) + ends);
             if (splits > 1) cost += 6000.0 + static_cast<double>(splits) * M * cols * 8 / 2000.0;
             if (cost < 0.97 * best_cost) {
                 best_cost = cost;
@@ -387,7 +394,8 @@ int rank_grad(const GroupCtx& c, bool is_b, const uint16_t* act, const uint16_t*
 // ------------------------------------------------------------------ fused products
 // m: the maps of k_group_gemm, those of the tokens (0 and 2) still to be made.
 struct FusedMaps {
-    CUtensorMap m[4];
+    RowMaps act_rows, pair_rows;
+    CUtensorMap codes, factor;
     const uint16_t *act, *pair;
     int64_t contraction, pair_cols, M;
 };
@@ -399,8 +407,10 @@ cudaError_t launch_group_gemm(const char* name, FusedMaps& f, GroupGemmArgs g, b
     static bool done[64] = {};
     const cudaError_t e = opt_in(reinterpret_cast<const void*>(&k_group_gemm<DX, T, DROP>), C::kSmem, done);
     if (e != cudaSuccess) return keep(e);
-    *mapped = map16(&f.m[0], f.act, f.contraction, f.M, 0, C::kSubT / 2) &&
-              map16(&f.m[2], f.pair, f.pair_cols, f.M, 0, C::kSubT / 2);
+    *mapped = true;
+    for (int i = 0; i < C::kBoxes; ++i)
+        *mapped = *mapped && map16(&f.act_rows.m[i], f.act, f.contraction, f.M, 0, C::kBoxRows * (i + 1)) &&
+                  map16(&f.pair_rows.m[i], f.pair, f.pair_cols, f.M, 0, C::kBoxRows * (i + 1));
     if (!*mapped) return cudaSuccess;
     const int64_t row_tiles = most_tiles(g.offsets, g.E, g.M, g.tile_rows);
     g.row_tiles = cols_fastest ? -1 : static_cast<int>(row_tiles);
@@ -412,8 +422,8 @@ cudaError_t launch_group_gemm(const char* name, FusedMaps& f, GroupGemmArgs g, b
     g.walk_fast = static_cast<int>(pairs / g.splits % fast);
     g.walk_slow = static_cast<int>(pairs / g.splits / fast);
     const dim3 grid(static_cast<unsigned>(2 * pairs));
-    return launch_clustered(name, k_group_gemm<DX, T, DROP>, grid, 2, C::kThreads, C::kSmem, st, f.m[0], f.m[1],
-                            f.m[2], f.m[3], g);
+    return launch_clustered(name, k_group_gemm<DX, T, DROP>, grid, 2, C::kThreads, C::kSmem, st, f.act_rows,
+                            f.codes, f.pair_rows, f.factor, g);
 }
 
 // Y (act X, pair T2, factor B) or dX (act dY, pair V2, factor A).
@@ -442,15 +452,15 @@ int fused(const GroupCtx& c, bool dx, const uint16_t* act, const uint16_t* pair,
     g.part = part;
     g.drop = c.drop;
     FusedMaps f;
-    std::memset(f.m, 0, sizeof(f.m));
+    std::memset(&f, 0, sizeof(f));
     f.act = act;
     f.pair = pair;
     f.contraction = contraction;
     f.pair_cols = 2 * r64;
     f.M = c.M;
-    if (dx ? !map_packed(&f.m[1], c.codes, c.N, c.K, c.E, 64, 64) || !map16(&f.m[3], factor, c.K, c.r, c.E, 64)
-           : !map_packed(&f.m[1], c.codes, c.N, c.K, c.E, 32, 128) ||
-                 !map16(&f.m[3], factor, ceil_to(c.r, 8), c.N, c.E, 128))
+    if (dx ? !map_packed(&f.codes, c.codes, c.N, c.K, c.E, 64, 64) || !map16(&f.factor, factor, c.K, c.r, c.E, 64)
+           : !map_packed(&f.codes, c.codes, c.N, c.K, c.E, 32, 128) ||
+                 !map16(&f.factor, factor, ceil_to(c.r, 8), c.N, c.E, 128))
         return -1;
     // The tiles that run together share what they re-read.  Column tiles
     // fastest reads the activations once and a group's weight once per token

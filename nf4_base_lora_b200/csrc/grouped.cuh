@@ -202,6 +202,40 @@ __device__ __forceinline__ void mma2_elect(uint32_t d_tmem, uint64_t a_desc, uin
         : "memory");
 }
 
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Four of them, 64 deep, issued by one elected lane; kA and kB: from one 16 of the
+// contraction to the next, in descriptor units.
+template <int kA, int kB>
+__device__ __forceinline__ void mma2_elect4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, t, e;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.s64 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 2 * %5;\n\tadd.s64 b, %2, 2 * %6;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 3 * %5;\n\tadd.s64 b, %2, 3 * %6;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kA), "n"(kB)
+        : "memory");
+}
+
 // The same with operand A in tensor memory: 128 lanes (rows) of each CTA by 8
 // columns, two bf16 of the contraction in a column.
 __device__ __forceinline__ void mma2_elect_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -353,6 +387,13 @@ struct GroupGemmArgs {
     DropArgs drop;           // input gradient with dropout only
 };
 
+// Tensor maps of the same rows with boxes of kBoxRows, 2 kBoxRows, ...: a tile's
+// copies bring the rows it has and not the largest tile's (the tokens' way from L2
+// is what bounds a tile of 352 tokens otherwise).
+struct RowMaps {
+    CUtensorMap m[4];
+};
+
 // T tokens per tile at most.  512: one CTA per SM, four teams, steps of 64; the
 // MMAs bound it.  32: the decode bounds it, so two CTAs per SM of two teams each,
 // whose starts and ends overlap, and steps of 128 (kKS = 2 units per thread),
@@ -375,6 +416,7 @@ struct GroupGemmConfig {
     static constexpr int kDS = T > 256 ? 4 : T > 64 || kWT ? 3 : 2;  // slots of decoded tiles and of tokens
     static constexpr int kLC = T > 256 ? 8 : T > 64 ? 4 : 2 * kDS;   // slots of packed codes
     static constexpr int kWS = kWT ? 1 : kDS;          // slots of weight tiles in shared memory (kWT: extension only)
+    static constexpr int kBoxRows = kSubT / 2 < 32 ? kSubT / 2 : 32, kBoxes = kSubT / 2 / kBoxRows;
     static constexpr int kSub = kSubT / 2 * 128;       // a CTA's tokens of one accumulator, 64 deep
     static constexpr int kTok = kSubs * kSub;          // of all accumulators
     static constexpr int kCodes = kBM * 32, kW = kBM * 128;  // a packed and a decoded tile, 64 deep
@@ -402,14 +444,14 @@ struct GroupGemmConfig {
     static_assert(kSub % 1024 == 0 && kSmem * kMinBlocks <= 226 * 1024, "shared memory");
 };
 
-// map_t: X [M, K] or dY [M, N], box {64, kSubT / 2}.  map_w: codes (K / 2, N,
+// map_t: X [M, K] or dY [M, N], boxes {64, kBoxRows ...}.  map_w: codes (K / 2, N,
 // E), box {32, 128, 1} (forward) or {64, 64, 1}.  map_te: T2 or V2 [M, 2 r64],
-// box {64, kSubT / 2}.  map_we: B (r, N, E), box {64, 128, 1} (forward) or A (K,
+// boxes as map_t's.  map_we: B (r, N, E), box {64, 128, 1} (forward) or A (K,
 // r, E), box {64, 64, 1}.  Cluster of two along grid.x.
 template <bool DX, int T, bool DROP>
 __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmConfig<DX, T>::kMinBlocks)
-    k_group_gemm(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_w,
-                 const __grid_constant__ CUtensorMap map_te, const __grid_constant__ CUtensorMap map_we,
+    k_group_gemm(const __grid_constant__ RowMaps map_t, const __grid_constant__ CUtensorMap map_w,
+                 const __grid_constant__ RowMaps map_te, const __grid_constant__ CUtensorMap map_we,
                  const GroupGemmArgs args) {
     using C = GroupGemmConfig<DX, T>;
     static_assert(DX || !DROP, "only the input gradient masks its accumulator");
@@ -587,9 +629,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
     if (warp == 0) {
         // ------------------------------------------------------------ copies
         if (lane == 0) {
-            tma_prefetch_desc(&map_t);
             tma_prefetch_desc(&map_w);
-            tma_prefetch_desc(&map_te);
             tma_prefetch_desc(&map_we);
         }
         __syncwarp();
@@ -618,6 +658,13 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
         bool stop = false;
         while (!stop && next_tile(wt, tt)) {
             const int n_iter = tt.n_main + tt.n_ext;
+            // the boxes that hold the rows this CTA brings for an accumulator
+            int box[C::kSubs], bytes = 0;
+#pragma unroll
+            for (int ms = 0; ms < C::kSubs; ++ms) {
+                box[ms] = min(max(0, ((sub_n(tt, ms) >> 1) - 1) / C::kBoxRows), C::kBoxes - 1);
+                if (ms < tt.nsub) bytes += C::kKS * (box[ms] + 1) * C::kBoxRows * 128;
+            }
             for (int it = 0; it < n_iter; ++it) {
                 // the step DS before is multiplied: its token and decode slots are
                 // free, and so is the code slot of the step kAhead ahead, which its
@@ -635,15 +682,17 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                 }
                 if (elect_one()) {
                     if (rank == 0)
-                        mbar_arrive_expect_tx(&bar_ready[ds], 2 * (C::kKS * tt.nsub * C::kSub + (main_step ? 0 : C::kWBytes)));
+                        mbar_arrive_expect_tx(&bar_ready[ds], 2 * (bytes + (main_step ? 0 : C::kWBytes)));
                     const uint32_t bar = lead(&bar_ready[ds]);
                     if (main_step) {
                         const int kb = (tt.kb0 + it - main0(tt)) * C::kKS;
 #pragma unroll
                         for (int h = 0; h < C::kKS; ++h)
-                            for (int ms = 0; ms < tt.nsub; ++ms)
-                                tma_load_2d_pair(t_buf(ds) + h * C::kTok + ms * C::kSub, &map_t, bar, (kb + h) * 64,
-                                                 sub_row(tt, ms));
+#pragma unroll
+                            for (int ms = 0; ms < C::kSubs; ++ms)
+                                if (ms < tt.nsub)
+                                    tma_load_2d_pair(t_buf(ds) + h * C::kTok + ms * C::kSub, &map_t.m[box[ms]], bar,
+                                                     (kb + h) * 64, sub_row(tt, ms));
                     } else {
                         // [hi | lo] against the factor twice
                         const int half = tt.n_ext * C::kKS / 2;
@@ -652,9 +701,11 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
 #pragma unroll
                         for (int h = 0; h < C::kKS; ++h) {
                             const int j = j0 + h, jb = j % half;
-                            for (int ms = 0; ms < tt.nsub; ++ms)
-                                tma_load_2d_pair(t_buf(ds) + h * C::kTok + ms * C::kSub, &map_te, bar, j * 64,
-                                                 sub_row(tt, ms));
+#pragma unroll
+                            for (int ms = 0; ms < C::kSubs; ++ms)
+                                if (ms < tt.nsub)
+                                    tma_load_2d_pair(t_buf(ds) + h * C::kTok + ms * C::kSub, &map_te.m[box[ms]], bar,
+                                                     j * 64, sub_row(tt, ms));
                             uint8_t* dst = w_buf(C::kWT ? j0 % C::kWS : ds) + h * C::kW;
                             if constexpr (DX) {
 #pragma unroll
@@ -697,6 +748,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             const uint32_t tmem_d = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
             bool stop = false;
             int n_masked = 0, ds = 0;
+            bool early = false;
             uint32_t ready = 0;
             Walk walk;
             first_tile(walk);
@@ -720,10 +772,13 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                     stop = !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_free[tl % C::kAccs], (tl / C::kAccs + 1) & 1u,
                                                               abort_flag));
                 for (int it = 0; it < n_iter && !stop; ++it) {
-                    // the tokens and the weight tiles of both CTAs are in place
-                    stop = !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_ready[ds], ready, abort_flag));
+                    // the tokens and the weight tiles of both CTAs are in place; the
+                    // next step's barrier is polled beside the MMAs' issue
+                    if (!early) stop = !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_ready[ds], ready, abort_flag));
                     if (stop) break;
                     tc_fence_after();
+                    const bool wrap = ds + 1 == DS;
+                    const bool next = mbar_test(&bar_ready[wrap ? 0 : ds + 1], wrap ? ready ^ 1u : ready);
                     const uint64_t td = t_desc0 + static_cast<uint32_t>(ds) * (C::kTokBytes / 16);
                     const uint32_t acc = it > 0 ? 1u : 0u;
                     if (C::kWT && it < n_main) {
@@ -736,15 +791,16 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                         const int ws = C::kWT ? (it - n_main) % C::kWS : ds;
                         const uint64_t wd = w_desc0 + static_cast<uint32_t>(ws) * (C::kWBytes / 16);
 #pragma unroll
-                        for (int k = 0; k < 4 * C::kKS; ++k) {
-                            const uint64_t w16 = wd + (k / 4) * (C::kW / 16) + (k % 4) * kWk;
-                            const uint64_t t16 = td + (k / 4) * (C::kTok / 16) + (k % 4) * kTk;
-                            mma2_elect(acc_d, w16, t16, idesc0, k > 0 ? 1u : acc);
+                        for (int h = 0; h < C::kKS; ++h) {
+                            const uint64_t w64 = wd + h * (C::kW / 16), t64 = td + h * (C::kTok / 16);
+                            mma2_elect4<kWk, kTk>(acc_d, w64, t64, idesc0, h > 0 ? 1u : acc);
                             if (C::kSubs == 2 && nsub == 2)
-                                mma2_elect(acc_d + C::kSubT, w16, t16 + C::kSub / 16, idesc1, k > 0 ? 1u : acc);
+                                mma2_elect4<kWk, kTk>(acc_d + C::kSubT, w64, t64 + C::kSub / 16, idesc1,
+                                                      h > 0 ? 1u : acc);
                         }
                     }
                     mma2_commit_elect(&bar_done[ds]);
+                    early = __all_sync(0xFFFFFFFFu, next);
                     if (DROP && it == ext_last) {
                         mma2_commit_elect(&bar_ext);
                         stop = !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_masked, n_masked++ & 1u, abort_flag));
