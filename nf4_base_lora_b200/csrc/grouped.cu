@@ -379,8 +379,8 @@ int rank_grad(const GroupCtx& c, bool is_b, const uint16_t* act, const uint16_t*
     if (e != cudaSuccess) return -2;
     if (parts == 1) return 0;
     const bool vec = !is_b || c.r % 4 == 0;
-    dim3 sum_grid = flat_grid(rows * c.r / (vec ? 4 : 1), c.num_sms);
-    sum_grid.y = static_cast<unsigned>(c.E);
+    const int64_t sum_blocks = c.E * div_up(rows * c.r / (vec ? 4 : 1), 256);
+    const dim3 sum_grid(static_cast<unsigned>(std::min<int64_t>(sum_blocks, 4 * c.num_sms)));
     auto sum = [&](auto kern) {
         return launch_dependent("rank_grad_sum", kern, sum_grid, 256, 0, c.stream, c.offsets, c.E, g.M, part_steps,
                                 g.slots, static_cast<const float*>(part), static_cast<int>(rows), c.r, g.rn, g.alpha,

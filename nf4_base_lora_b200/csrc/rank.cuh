@@ -95,6 +95,9 @@ struct RankConfig {
 
 // The parts of the groups' rows for dB and dA, numbered in group order: a group
 // has ceil(rows / (64 part_steps)) of them, at least one.
+__device__ __forceinline__ int rank_parts(int n, int part_steps) {
+    return max(1, (n + 64 * part_steps - 1) / (64 * part_steps));
+}
 struct RankPart {
     int e;
     int begin, end;  // the group's rows
@@ -102,21 +105,18 @@ struct RankPart {
     int part;        // this one
     int slot;        // of the group's first partial; groups of one part take none
 };
-// Part u (its group's first one where FIRST: u counts groups); the whole warp
-// calls it.  False beyond the last.  A group beyond the last slot, which only
+// Part u; the whole warp calls it.  False beyond the last.  A group beyond the last slot, which only
 // offsets that break their rule can make, stays whole (its later parts are void).
-template <bool FIRST>
 __device__ __forceinline__ bool find_part(const int32_t* offsets, int E, int M, int part_steps, int slots, int u,
                                           int lane, RankPart& p) {
-    auto count = [&](int n) { return max(1, (n + 64 * part_steps - 1) / (64 * part_steps)); };
     p.slot = 0;
     if (offsets == nullptr) {
         p.e = 0;
         p.begin = 0;
         p.end = M;
-        p.parts = count(M);
-        p.part = FIRST ? 0 : u;
-        return p.part < p.parts && (!FIRST || u == 0);
+        p.parts = rank_parts(M, part_steps);
+        p.part = u;
+        return p.part < p.parts;
     }
     int before = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {
@@ -124,10 +124,10 @@ __device__ __forceinline__ bool find_part(const int32_t* offsets, int E, int M, 
         int begin = 0, end = 0, n = 0;
         if (e < E) {
             group_bounds(offsets, e, M, begin, end);
-            n = count(end - begin);
+            n = rank_parts(end - begin, part_steps);
         }
-        const int taken = n > 1 ? n : 0, units = FIRST ? (e < E ? 1 : 0) : n;
-        int incl = units, sl = taken;
+        const int taken = n > 1 ? n : 0;
+        int incl = n, sl = taken;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d), w = __shfl_up_sync(0xFFFFFFFFu, sl, d);
@@ -143,7 +143,7 @@ __device__ __forceinline__ bool find_part(const int32_t* offsets, int E, int M, 
             p.begin = __shfl_sync(0xFFFFFFFFu, begin, src);
             p.end = __shfl_sync(0xFFFFFFFFu, end, src);
             p.parts = __shfl_sync(0xFFFFFFFFu, n, src);
-            p.part = FIRST ? 0 : u - before - __shfl_sync(0xFFFFFFFFu, incl - units, src);
+            p.part = u - before - __shfl_sync(0xFFFFFFFFu, incl - n, src);
             p.slot += __shfl_sync(0xFFFFFFFFu, sl - taken, src);
             if (p.parts > 1 && p.slot + p.parts > slots) p.parts = 1;
             return p.part < p.parts;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
         step0 = blockIdx.z * args.k_per_split;
         n_steps = min(args.k_per_split, args.k_steps - step0);
     } else {
-        if (!find_part<false>(args.offsets, args.E, args.M, args.part_steps, args.slots, blockIdx.y, lane, part))
+        if (!find_part(args.offsets, args.E, args.M, args.part_steps, args.slots, blockIdx.y, lane, part))
             return;
         g.e = part.e;
         begin = part.begin;
@@ -568,37 +568,88 @@ __global__ void k_rank_pair(const float* __restrict__ src, int64_t M, int r, int
 }
 
 // dB [E][N][r] (TRANSPOSED false) or dA [E][r][K] of the groups of several parts,
-// from partials [part][N][rn] or [part][rn][K], added in order.  grid.y: expert.
-// VEC elements at a time (4 needs r to be a multiple of 4 where not TRANSPOSED).
+// from partials [part][N][rn] or [part][rn][K], added in order.  Each block lists
+// those groups first and takes its share of their elements, so that the many
+// groups of one part cost nothing (a block per expert: 18 and 23 us for 64 experts
+// of 2048 x 1408, of which a few have several parts).  VEC elements at a time (4
+// needs r to be a multiple of 4 where not TRANSPOSED).
+constexpr int kSumExperts = 4096;
 template <bool TRANSPOSED, int VEC>
 __global__ void __launch_bounds__(256)
     k_rank_grad_sum(const int32_t* offsets, int E, int M, int part_steps, int slots, const float* __restrict__ part,
                     int rows, int r, int rn, float alpha, uint16_t* __restrict__ out, int accumulate) {
+    __shared__ int s_slot[kSumExperts], s_parts[kSumExperts], s_warp[8][2];
+    __shared__ uint16_t s_e[kSumExperts];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // the offsets were complete before the kernels that this one follows
+    int groups = 0, slot0 = 0;
+    for (int e0 = 0; e0 < E; e0 += 256) {
+        const int e = e0 + threadIdx.x;
+        int begin = 0, end = 0;
+        if (e < E) {
+            if (offsets != nullptr) group_bounds(offsets, e, M, begin, end);
+            else end = M;
+        }
+        const int n = rank_parts(end - begin, part_steps), taken = n > 1 ? n : 0;
+        int g = n > 1 ? 1 : 0, sl = taken;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, g, d), w = __shfl_up_sync(0xFFFFFFFFu, sl, d);
+            if (lane >= d) {
+                g += v;
+                sl += w;
+            }
+        }
+        if (lane == 31) {
+            s_warp[warp][0] = g;
+            s_warp[warp][1] = sl;
+        }
+        __syncthreads();
+        int g_all = 0, sl_all = 0;
+        for (int w = 0; w < 8; ++w) {
+            if (w == warp) {
+                g += g_all;
+                sl += sl_all;
+            }
+            g_all += s_warp[w][0];
+            sl_all += s_warp[w][1];
+        }
+        if (n > 1) {
+            s_e[groups + g - 1] = static_cast<uint16_t>(e);
+            s_slot[groups + g - 1] = slot0 + sl - taken;
+            // what the slots do not hold was written as one part (offsets that
+            // break their contract)
+            s_parts[groups + g - 1] = slot0 + sl <= slots ? n : 0;
+        }
+        groups += g_all;
+        slot0 += sl_all;
+        __syncthreads();
+    }
     grid_dependency_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    RankPart p;
-    if (!find_part<true>(offsets, E, M, part_steps, slots, blockIdx.y, threadIdx.x & 31, p) || p.parts == 1) return;
     const int64_t slice = static_cast<int64_t>(rows) * rn;
     const int inner = (TRANSPOSED ? rows : r) / VEC, ld = TRANSPOSED ? rows : rn;
-    const int64_t total = static_cast<int64_t>(rows) * r / VEC;
-    const float* src = part + p.slot * slice;
-    uint16_t* dst = out + static_cast<int64_t>(p.e) * rows * r;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t total = static_cast<int64_t>(rows) * r / VEC, chunks = (total + 255) / 256;
+    for (int64_t u = blockIdx.x; u < groups * chunks; u += gridDim.x) {
+        const int k = static_cast<int>(u / chunks), parts = s_parts[k];
+        const int64_t i = (u - k * chunks) * 256 + threadIdx.x;
+        if (parts == 0 || i >= total) continue;
+        uint16_t* dst = out + static_cast<int64_t>(s_e[k]) * rows * r;
         const int64_t outer = total < (int64_t(1) << 31) ? static_cast<int>(i) / inner : i / inner;
-        const float* at = src + outer * ld + (i - outer * inner) * VEC;
+        const float* at = part + s_slot[k] * slice + outer * ld + (i - outer * inner) * VEC;
         float v[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) v[j] = 0.0f;
-        for (int z = 0; z < p.parts; ++z, at += slice) {
+#pragma unroll 4
+        for (int z = 0; z < parts; ++z) {
             if constexpr (VEC == 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(at));
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(at + z * slice));
                 v[0] += x.x;
                 v[1] += x.y;
                 v[2] += x.z;
                 v[3] += x.w;
             } else {
-                v[0] += __ldcg(at);
+                v[0] += __ldcg(at + z * slice);
             }
         }
 #pragma unroll
