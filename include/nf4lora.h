@@ -326,7 +326,9 @@ int qlora_linear_dropout_bwd(const nf4_tensor* w, const uint16_t* A, const uint1
  * tiles that M rows in n_experts groups can need.
  * Offsets that break the rule lead no access out of the arrays; the results
  * are then undefined, and nf4lora_device_status() returns NF4_ERR_INVALID_ARG.
- * Requirements: 1 <= n_experts <= NF4_MAX_EXPERTS, d_out % 8 == 0; else as for
+ * Requirements: 1 <= n_experts <= NF4_MAX_EXPERTS, d_out % 8 == 0,
+ * n_experts * d_out * d_in / 64 < 2^32; no output overlaps an input or another
+ * output; else as for
  * qlora_linear_fwd / _bwd, ws >= the sizes below (d_out of one expert).
  */
 size_t qlora_grouped_fwd_workspace_bytes(int64_t M, int n_experts, int64_t d_out, int64_t d_in, int r);

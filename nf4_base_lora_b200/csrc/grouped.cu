@@ -154,9 +154,13 @@ Split split_steps(int64_t tiles, int64_t steps, int ctas) {
 int rank_width(int r) { return static_cast<int>(ceil_to(r, 16)); }
 int rank64(int r) { return static_cast<int>(ceil_to(r, 64)); }
 
-// Contraction splits of T (steps over K) and V (over N): two CTAs per SM.
+// Contraction splits of T (steps over K) and V (over N): two CTAs per SM.  A tile
+// for every SM is enough, though: halves would only add their sum (16000 tokens
+// over 64 experts of 2048 x 1408, step: 454 us with two parts, 438 with one).
 Split rows_split(int E, int64_t M, int64_t contraction, int num_sms) {
-    return split_steps(likely_tiles(E, M, 128), div_up(contraction, 64), 2 * num_sms);
+    const int64_t tiles = likely_tiles(E, M, 128), steps = div_up(contraction, 64);
+    if (tiles >= num_sms) return {1, static_cast<int>(steps)};
+    return split_steps(tiles, steps, 2 * num_sms);
 }
 
 // Steps of a part of a group's rows for dB (out rows N) and dA (out rows K): so

@@ -122,3 +122,12 @@ def test_binding_refuses_tensors_of_the_wrong_kind(nf):
         nf.lora_dropout(x, 0.1, None)                             # not on a GPU
     with pytest.raises(ValueError):
         nf.lora_dropout(x.half(), 0.1, None)
+
+
+def test_a_weight_of_too_many_blocks_is_refused(nf):
+    w = weight(nf, 1 << 23, 1 << 15)                              # 2^32 blocks of 64
+    assert fwd(nf, w) == SHAPE and gfwd(nf, w) == SHAPE and gbwd(nf, w) == SHAPE
+    assert nf.qlora_grouped_fwd_workspace_bytes(16, 2, 1 << 22, 1 << 15, 8) == 0
+    w = weight(nf, (1 << 23) - 16, 1 << 15)
+    assert fwd(nf, w) == CUDA and gfwd(nf, w) == CUDA             # passes the checks, no device here
+    assert nf.qlora_grouped_fwd_workspace_bytes(16, 2, (1 << 22) - 8, 1 << 15, 8) > 0

@@ -48,6 +48,12 @@ CASES = [
     (6, 1408, 2048, 8, [400, 0, 129, 257, 1000, 6], 5, 0, 0.1, False),
     (8, 4096, 1088, 16, [10, 2, 0, 0, 1, 8, 16, 27], 0, 0, 0.0, True),      # serving, some above 16 rows
     (8, 1096, 4160, 16, [1, 0, 0, 1, 0, 0, 0, 0], 0, 0, 0.0, True),         # one token, two experts
+    (130, 72, 128, 8, [(5 * i) % 61 for i in range(130)], 2, 1, 0.1, True),  # more groups than a kernel keeps, 256-token tiles
+    (140, 72, 192, 8, [i % 4 for i in range(140)], 0, 3, 0.1, True),         # and 32-token ones
+    (300, 64, 64, 8, [0] * 150 + [1200] + [1] * 148 + [700], 0, 0, 0.1, True),  # long groups far apart: summed parts
+    (4096, 8, 64, 4, [1 if i % 3 else 0 for i in range(4096)], 0, 7, 0.0, True),  # most experts
+    (2, 264, 192, 256, [600, 515], 0, 0, 0.25, True),                        # 512-token tiles, largest rank
+    (2, 328, 448, 32, [505, 33], 1, 2, 0.0, False),                          # an odd number of blocks
 ]
 
 
@@ -217,3 +223,86 @@ def test_an_empty_batch(nf):
     _, dA, dB = nf.qlora_grouped_bwd(w, d["A"], d["B"], 1.0, d["X"], None, d["dY"], offsets)
     torch.cuda.synchronize()
     assert (Y == 3.0).all() and not dA.any() and not dB.any()
+
+
+@pytest.mark.parametrize("tokens", [40, 700])
+def test_a_mixture_trains_as_its_parts_say(nf, tokens):
+    """Routing, two grouped layers with adapter dropout, their backward and the
+    optimizer, as a training step runs them: every stage within its bounds of the
+    64-bit result for the inputs it had, nothing read back to the host between
+    them, and the same step replayed from a graph."""
+    E, D, F, r, top, p = 6, 192, 320, 8, 2, 0.1
+    M = tokens * top
+    g = torch.Generator(device="cuda").manual_seed(11)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda")
+    up, down = (nf.nf4_quantize(rn(E * n, k) * 0.05) for n, k in ((F, D), (D, F)))
+    Wu, Wd = nf.nf4_dequantize(up).reshape(E, F, D), nf.nf4_dequantize(down).reshape(E, D, F)
+    master = [rn(E, r, D) / r, rn(E, F, r) * 0.05, rn(E, r, F) / r, rn(E, D, r) * 0.05]
+    start = [m.clone() for m in master]
+    param = [m.bfloat16() for m in master]
+    moments = [(torch.zeros_like(m), torch.zeros_like(m)) for m in master]
+    x, target, router = rn(tokens, D).bfloat16(), rn(tokens, D).bfloat16(), rn(D, E).bfloat16()
+    rng = torch.tensor([77, 0], dtype=torch.int64, device="cuda")
+    rng2 = torch.tensor([78, 0], dtype=torch.int64, device="cuda")
+    s = 1.5
+    seen = {}
+
+    def step():
+        gate, expert = (x @ router).float().softmax(-1).topk(top)
+        flat, order = expert.flatten().sort(stable=True)
+        offsets = torch.searchsorted(flat, torch.arange(E + 1, device="cuda"), out_int32=True)
+        token = order // top
+        xs = x[token].contiguous()
+        h, t1 = nf.qlora_grouped_fwd(up, param[0], param[1], s, xs, offsets, p, rng)
+        a = torch.nn.functional.silu(h.float()).bfloat16()
+        y, t2 = nf.qlora_grouped_fwd(down, param[2], param[3], s, a, offsets, p, rng2)
+        scale = gate.flatten()[order].unsqueeze(1)
+        out = torch.zeros(tokens, D, device="cuda").index_add_(0, token, y.float() * scale)
+        dy = ((out - target.float())[token] * scale).bfloat16()
+        da, dA2, dB2 = nf.qlora_grouped_bwd(down, param[2], param[3], s, a, t2, dy, offsets, p, rng2)
+        sig = h.float().sigmoid()
+        dh = (da.float() * sig * (1 + h.float() * (1 - sig))).bfloat16()
+        dx, dA1, dB1 = nf.qlora_grouped_bwd(up, param[0], param[1], s, xs, t1, dh, offsets, p, rng)
+        seen.update(off=offsets, xs=xs, h=h, t1=t1, a=a, y=y, t2=t2, dy=dy, da=da, dh=dh, dx=dx,
+                    grads=[dA1, dB1, dA2, dB2], before=[q.clone() for q in param])
+        nf.lora_adamw_step([(m, q, d, *v) for m, q, d, v in zip(master, param, seen["grads"], moments)], 1e-3)
+
+    def verify():
+        torch.cuda.synchronize()
+        nf.device_status()
+        off = seen["off"].tolist()
+        assert off[0] == 0 and off[-1] == M
+        b, gr = seen["before"], seen["grads"]
+        one = reference(Wu, b[0], b[1], seen["xs"], seen["dh"], off, s, p, (77, 0))
+        two = reference(Wd, b[2], b[3], seen["a"], seen["dy"], off, s, p, (78, 0))
+        for ref, got in ((one, (seen["t1"], seen["h"], seen["dx"], gr[0], gr[1])),
+                         (two, (seen["t2"], seen["y"], seen["da"], gr[2], gr[3]))):
+            for name, v in zip(("T", "Y", "dX", "dA", "dB"), got):
+                check(v, ref, name)
+
+    def reset():
+        for m, m0, q, (m1, m2) in zip(master, start, param, moments):
+            m.copy_(m0)
+            q.copy_(m0)
+            m1.zero_()
+            m2.zero_()
+
+    step()
+    verify()
+    eager = [m.clone() for m in master] + [seen["dx"].clone(), seen["y"].clone()]
+    assert all((m != m0).any() for m, m0 in zip(master, start))
+    reset()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(2):
+        reset()
+        graph.replay()
+        verify()
+        # the sums of the routed outputs add in any order, all else in one
+        assert torch.equal(seen["y"], eager[-1])
+    x.copy_(rn(tokens, D))  # other tokens, other offsets
+    reset()
+    graph.replay()
+    verify()
