@@ -15,11 +15,12 @@
 // token and of thousands.
 //
 // The pairs are persistent: pair i takes the tiles i, i + pairs, ... and keeps
-// its barriers, rings and tensor memory; the copies of the next tile run while
-// the epilogue of the last one empties the accumulators.  The groups' bounds are
-// device data: each warp finds a tile by a scan of the offsets, and the first
-// tile beyond the last group ends the walk.  A group of n rows is divided evenly
-// into tiles of at most tile_rows.  A tile never crosses a group: rows of the
+// its barriers, rings and tensor memory; the copies and decodes of the next tile
+// run while the epilogue of the last one empties the accumulators.  The groups'
+// bounds are device data: a CTA lists them once (up to 127 groups; beyond, each
+// warp finds its tiles by scans of the offsets), and the first tile beyond the
+// last group ends the walk.  A group of n rows is divided evenly into tiles of at
+// most tile_rows.  A tile never crosses a group: rows of the
 // next group that its copies bring in are accumulator columns that are not
 // stored, or beyond N altogether.  With few tokens the contraction is split too
 // (fp32 partials, added in order by k_group_sum), so that the tiles divide evenly
@@ -30,14 +31,20 @@
 // a NaN or an infinity in one expert's adapter cannot reach another's result.
 //
 // Warp roles, in each CTA: warp 0 copies (TMA); warp 1 owns tensor memory and in
-// the leading CTA issues the MMAs; teams of four warps decode k-steps in turn
-// (one (weight row, block) unit per thread, register codebook) and run the
-// epilogue.  Three rings: tokens, packed codes (a few steps further ahead, so
-// that a decode never waits behind the tokens) and decoded tiles.  One barrier of
-// the leading CTA collects, for a step, the bytes of both CTAs' tokens and both
-// teams' arrivals: the issuing thread waits once a step.  The rank-r term enters
-// the same accumulator as extension k-steps over [hi | lo] of the 16-bit pair of
-// T or V.
+// the leading CTA issues the MMAs; teams of four or eight warps decode k-steps in
+// turn and run the epilogue; with one CTA per SM a last warp copies the packed
+// codes.  Rings: steps (tokens and decoded tiles) and packed codes.  One barrier
+// of the leading CTA collects, for a step, the bytes of both CTAs' tokens and both
+// teams' arrivals: the issuing warp waits once a step, and polls the next step's
+// barrier beside the MMAs.  The rank-r term enters the same accumulator as
+// extension k-steps over [hi | lo] of the 16-bit pair of T or V.
+//
+// What bounds it (B200, CUDA graph, whole calls): many tokens, the tensor pipe
+// (4096 tokens, 4096 -> 11008: 249 us, 1480 TFLOP/s); a couple of hundred tokens a
+// group, the decode, 850 clocks a 64-deep step of which the integer or the
+// shared-memory pipe needs 300 to 500 and latencies of the decoding warps the
+// rest; few tokens, the decode too (64 tokens over eight experts of 4096 x 11008:
+// 105 us for 186 MB of codes and scales).
 //
 // Dropout (input gradient): the extension steps come first, the epilogue warps
 // read the accumulators back, keep and scale them in fp32 and store them to
@@ -301,12 +308,18 @@ __device__ __forceinline__ void tmem2_dealloc(uint32_t taddr, uint32_t ncols) {
 }
 
 // ------------------------------------------------------------------ decode
-// One (weight row, 64-block) unit: 32 packed bytes to 64 bf16, written as the 8
-// swizzled 16-byte chunks of one 128-byte row (dst: the row's address with the
-// swizzle's XOR already in it).  The look-up is that of csrc/decode.cuh with the
-// selectors formed for a whole code word; the byte permutes and logic run on the
-// integer pipe at half rate and are what the decode is bound by, so the shifts
-// are written as high halves of products, which run on the multiply pipe.
+// One (weight row, 64-block) unit: 32 packed bytes to 64 bf16.  Two look-ups:
+//
+// decode_word, eight codes by byte permutes: that of csrc/decode.cuh with the
+// selectors formed for a whole code word; the permutes and logic run on the
+// integer pipe at half rate and bound it, so the shifts are written as high
+// halves of products, which run on the multiply pipe.  370 clocks per SM for the
+// units of four warps.
+//
+// shuffle_word: each level comes from the lane that holds it (`level`: of this
+// lane's index modulo 16), and the products are rounded as they come, which needs
+// no table and no logic but takes the shared-memory pipe: 252 clocks (look-ups in
+// shared memory: 293; mixtures of the two: in between).
 __device__ __forceinline__ void decode_word(uint32_t w, const uint32_t (&P)[4], const uint32_t (&H)[4], uint32_t* o) {
     const uint32_t sel = w & 0x77777777u;                                          // index within 0-7 / 8-15
     const uint32_t pick = (__umulhi(w, 0x80000000u) & 0x44444444u) | 0x32103210u;  // from 8-15 if bit 3
@@ -320,9 +333,25 @@ __device__ __forceinline__ void decode_word(uint32_t w, const uint32_t (&P)[4], 
     }
 }
 
-__device__ __forceinline__ void decode_row(const uint8_t* src, float s, uint8_t* dst) {
+__device__ __forceinline__ void shuffle_word(uint32_t w, float s, float level, uint32_t* o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float even = __shfl_sync(0xFFFFFFFFu, level, w >> (8 * i + 4), 16);
+        const float odd = __shfl_sync(0xFFFFFFFFu, level, w >> 8 * i, 16);
+        o[i] = pack_bf16x2(__fmul_rn(even, s), __fmul_rn(odd, s));
+    }
+}
+
+// A unit as the 8 swizzled 16-byte chunks of one 128-byte row (dst: the row's
+// address with the swizzle's XOR already in it); the whole warp calls it.  Tiles
+// of up to 256 tokens take the shuffles (125 tokens in each of 64 experts of
+// 2048 x 1408, a training step: 295 us against 301), the larger ones, whose MMAs
+// and copies need the shared-memory pipe, the permutes (188 tokens in each of
+// eight of 4096 x 11008: 390 against 402).
+template <bool SHUFFLE>
+__device__ __forceinline__ void decode_row(const uint8_t* src, float s, float level, uint8_t* dst) {
     uint32_t P[4], H[4];
-    nf4_table(s, P, H);
+    if constexpr (!SHUFFLE) nf4_table(s, P, H);
     const uint4 c0 = *reinterpret_cast<const uint4*>(src);
     const uint4 c1 = *reinterpret_cast<const uint4*>(src + 16);
     const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
@@ -330,19 +359,17 @@ __device__ __forceinline__ void decode_row(const uint8_t* src, float s, uint8_t*
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         uint32_t o[4];
-        decode_word(words[j], P, H, o);
+        if constexpr (SHUFFLE) shuffle_word(words[j], s, level, o);
+        else decode_word(words[j], P, H, o);
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (j << 4)), "r"(o[0]), "r"(o[1]), "r"(o[2]),
                      "r"(o[3])
                      : "memory");
     }
 }
 
-// The same unit into tensor memory: 32 columns of the thread's lane from `taddr`
-// on (the warp's lane base in it), two weights a column; the whole warp calls it,
-// and waits for the stores itself.  The look-up is a shuffle from the lane that
-// holds the level (`level`: of this lane's index modulo 16), which needs no table
-// and no logic: 252 clocks per SM for the units of four warps, where byte permutes
-// take 370 (and look-ups in shared memory 293); mixtures lie in between.
+// A unit in tensor memory: 32 columns of the thread's lane from `taddr` on (the
+// warp's lane base in it), two weights a column; the whole warp calls it, and
+// waits for the stores itself.
 __device__ __forceinline__ void decode_lane(const uint8_t* src, float s, float level, uint32_t taddr) {
     const uint4 c0 = *reinterpret_cast<const uint4*>(src);
     const uint4 c1 = *reinterpret_cast<const uint4*>(src + 16);
@@ -350,14 +377,8 @@ __device__ __forceinline__ void decode_lane(const uint8_t* src, float s, float l
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
         uint32_t o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t w = words[j + i / 4];
-            const int b = 8 * (i % 4);
-            const float even = __shfl_sync(0xFFFFFFFFu, level, w >> (b + 4), 16);
-            const float odd = __shfl_sync(0xFFFFFFFFu, level, w >> b, 16);
-            o[i] = pack_bf16x2(__fmul_rn(even, s), __fmul_rn(odd, s));
-        }
+        shuffle_word(words[j], s, level, o);
+        shuffle_word(words[j + 1], s, level, o + 4);
         tmem_st_32x32b_x8(taddr + 4 * j, o);
     }
 }
@@ -388,22 +409,28 @@ struct GroupGemmArgs {
 };
 
 // Tensor maps of the same rows with boxes of kBoxRows, 2 kBoxRows, ...: a tile's
-// copies bring the rows it has and not the largest tile's (the tokens' way from L2
-// is what bounds a tile of 352 tokens otherwise).
+// copies bring the rows it has and not the largest tile's.
 struct RowMaps {
     CUtensorMap m[4];
 };
 
-// T tokens per tile at most.  512: one CTA per SM, four teams, steps of 64; the
-// MMAs bound it.  32: the decode bounds it, so two CTAs per SM of two teams each,
-// whose starts and ends overlap, and steps of 128 (kKS = 2 units per thread),
-// which halve the waits, arrivals and turns of the copying and issuing warps per
-// decoded weight (steps of 64: 167 us for 64 tokens over eight experts of
-// 4096 x 11008, steps of 128: 143 us).  Forward (kWT): the tile is K-major, lane =
-// weight row, and goes to tensor memory (32 columns a unit; three steps fit beside
-// the accumulators), by which the shared-memory pipe is free to do the look-ups as
-// shuffles (decode_lane): 107-112 us.  Input gradient: the tile is MN-major, which
-// only shared memory can hold.
+// T tokens per tile at most.
+//
+// 512: one CTA per SM, four teams, steps of 64, one set of accumulators; the MMAs,
+// and with fewer than 350 tokens their issue, bound it.
+//
+// 256: the decode bounds it; steps of 128 by teams of eight warps (half the waits,
+// arrivals and turns of the copying and issuing warps per decoded weight) and two
+// sets of accumulators, so that MMAs run beside the epilogue.  125 tokens in each
+// of 64 experts of 2048 x 1408, a training step: 328 us against 345 with 512.
+//
+// 32: two CTAs per SM of two teams each, whose starts and ends overlap, and steps
+// of 128 (two units per thread; steps of 64: 167 us for 64 tokens over eight
+// experts of 4096 x 11008, steps of 128: 143 us).  Forward (kWT): the tile is
+// K-major, lane = weight row, and goes to tensor memory (32 columns a unit; three
+// steps fit beside the accumulators), by which the shared-memory pipe is free to
+// do the look-ups as shuffles: 105 us.  Input gradient: the tile is MN-major,
+// which only shared memory can hold.
 template <bool DX, int T>
 struct GroupGemmConfig {
     static constexpr int kBM = 128;                    // weight columns of one CTA
@@ -901,7 +928,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
         // (into tensor memory a warp writes the lanes of its own quadrant)
         const int dt = C::kWT ? q * 32 + lane : (threadIdx.x - 64) % C::kBM;
         const int half = C::kKS > C::kUnits ? (threadIdx.x - 64) / C::kBM % (C::kKS / C::kUnits) : 0;
-        float level = 0.0f;  // of decode_lane
+        float level = 0.0f;  // of shuffle_word
 #pragma unroll
         for (int i = 0; i < 16; ++i) level = (lane & 15) == i ? nf4_level(i) : level;
         const bool fp32_scales = args.absmax != nullptr;  // no double quantisation
@@ -1118,7 +1145,8 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             } else if (main_step) {
 #pragma unroll
                 for (int h = 0; h < C::kUnits; ++h)
-                    decode_row(codes_buf(cs) + h * C::kCodes + code_off, sc[h], w_buf(ds) + h * C::kW + dst_off);
+                    decode_row<(T <= 256)>(codes_buf(cs) + h * C::kCodes + code_off, sc[h], level,
+                                           w_buf(ds) + h * C::kW + dst_off);
             }
             if (!C::kWT) fence_proxy_async_smem();
             __syncwarp();
