@@ -188,22 +188,22 @@ int64_t most_partials(int E, int64_t M, int part_steps) {
 // of 4096 x 11008: 1570 against 1295.
 // The groups are taken as equal, which the host has to.
 struct FusedPlan {
-    int tile;       // the kernel: tiles of up to 32 (two CTAs per SM), 256 or 512 tokens
+    int tile;       // the kernel: tiles of up to 32 or 64 (two CTAs per SM), 256 or 512 tokens
     int tile_rows;
     int splits;
     int k_main, k_ext;  // steps
 };
 
-FusedPlan plan_fused(int E, int64_t M, int64_t cols, int64_t contraction, int r, int num_sms) {
+FusedPlan plan_fused(bool dx, int E, int64_t M, int64_t cols, int64_t contraction, int r, int num_sms) {
     const int64_t groups = std::min<int64_t>(E, M), mean = div_up(M, groups), col_tiles = div_up(cols, 256);
     FusedPlan best{};
-    const bool few = mean <= 24;
+    const bool few = mean <= (dx ? 24 : 64);
     double best_cost = 1e30;
     const int64_t pairs = num_sms / 2 * (few ? 2 : 1);
-    for (int rows = few ? 32 : 512; rows >= 32; rows -= 32) {
+    for (int rows = !few ? 512 : dx ? 32 : 64; rows >= 32; rows -= 32) {
         const int64_t per_group = div_up(mean, rows), size = ceil_to(div_up(mean, per_group), 32);
         const int64_t tiles = groups * per_group * col_tiles;
-        const int tile = few ? 32 : rows <= 256 ? 256 : 512, wide = tile == 512 ? 64 : 128;
+        const int tile = few ? (dx ? 32 : 64) : rows <= 256 ? 256 : 512, wide = tile == 512 ? 64 : 128;
         const int k_main = static_cast<int>(div_up(contraction, wide)), k_ext = 2 * rank64(r) / wide;
         const double step = few           ? 1500.0
                             : tile == 256 ? 1520.0 + 1.2 * size
@@ -252,7 +252,7 @@ Workspace layout(uint8_t* base, int64_t M, int E, int64_t N, int64_t K, int r, i
     // apart from the rank-r partials, whose sum may still run when the fused
     // product's first tiles end
     const int64_t cols = backward ? K : N;
-    const FusedPlan f = plan_fused(E, M, cols, backward ? N : K, r, num_sms);
+    const FusedPlan f = plan_fused(backward, E, M, cols, backward ? N : K, r, num_sms);
     if (f.splits > 1) w.fused_part = reinterpret_cast<float*>(take(f.splits * M * cols * 4));
     w.bytes = off;
     return w;
@@ -435,7 +435,7 @@ int fused(const GroupCtx& c, bool dx, const uint16_t* act, const uint16_t* pair,
           uint16_t* out) {
     const int64_t contraction = dx ? c.N : c.K, cols = dx ? c.K : c.N;
     const int r64 = rank64(c.r);
-    const FusedPlan plan = plan_fused(c.E, c.M, cols, contraction, c.r, c.num_sms);
+    const FusedPlan plan = plan_fused(dx, c.E, c.M, cols, contraction, c.r, c.num_sms);
     GroupGemmArgs g{};
     g.offsets = c.offsets;
     g.E = c.E;
@@ -473,18 +473,23 @@ int fused(const GroupCtx& c, bool dx, const uint16_t* act, const uint16_t* pair,
     const bool cols_fastest = c.offsets != nullptr || 2 * c.M * contraction > c.N * c.K * 33 / 64;
     const bool drop = dx && c.drop.threshold != 0;
     bool mapped = false;
-    auto go = [&](auto t) {
+    auto go = [&](auto dir, auto t) {
+        constexpr bool DX = decltype(dir)::value;
         constexpr int T = decltype(t)::value;
-        return !dx    ? launch_group_gemm<false, T, false>("group_gemm_fwd", f, g, cols_fastest, c.num_sms, &mapped,
-                                                           c.stream)
-               : drop ? launch_group_gemm<true, T, true>("group_gemm_dx_drop", f, g, cols_fastest, c.num_sms, &mapped,
-                                                         c.stream)
-                      : launch_group_gemm<true, T, false>("group_gemm_dx", f, g, cols_fastest, c.num_sms, &mapped,
-                                                          c.stream);
+        if constexpr (DX)
+            if (drop)
+                return launch_group_gemm<true, T, true>("group_gemm_dx_drop", f, g, cols_fastest, c.num_sms, &mapped,
+                                                        c.stream);
+        return launch_group_gemm<DX, T, false>(DX ? "group_gemm_dx" : "group_gemm_fwd", f, g, cols_fastest, c.num_sms,
+                                               &mapped, c.stream);
     };
-    cudaError_t e = plan.tile == 32    ? go(std::integral_constant<int, 32>())
-                    : plan.tile == 256 ? go(std::integral_constant<int, 256>())
-                                       : go(std::integral_constant<int, 512>());
+    auto pick = [&](auto dir) {
+        constexpr int kFew = decltype(dir)::value ? 32 : 64;
+        return plan.tile == kFew  ? go(dir, std::integral_constant<int, kFew>())
+               : plan.tile == 256 ? go(dir, std::integral_constant<int, 256>())
+                                  : go(dir, std::integral_constant<int, 512>());
+    };
+    cudaError_t e = dx ? pick(std::true_type()) : pick(std::false_type());
     if (e != cudaSuccess) return -2;
     if (!mapped) return -1;
     if (plan.splits > 1) {

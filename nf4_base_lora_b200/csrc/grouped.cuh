@@ -424,13 +424,15 @@ struct RowMaps {
 // sets of accumulators, so that MMAs run beside the epilogue.  125 tokens in each
 // of 64 experts of 2048 x 1408, a training step: 328 us against 345 with 512.
 //
-// 32: two CTAs per SM of two teams each, whose starts and ends overlap, and steps
-// of 128 (two units per thread; steps of 64: 167 us for 64 tokens over eight
-// experts of 4096 x 11008, steps of 128: 143 us).  Forward (kWT): the tile is
-// K-major, lane = weight row, and goes to tensor memory (32 columns a unit; three
-// steps fit beside the accumulators), by which the shared-memory pipe is free to
-// do the look-ups as shuffles: 105 us.  Input gradient: the tile is MN-major,
-// which only shared memory can hold.
+// 64 (forward), 32 (input gradient): two CTAs per SM of two teams each, whose
+// starts and ends overlap, and steps of 128 (two units per thread; steps of 64:
+// 167 us for 64 tokens over eight experts of 4096 x 11008, steps of 128: 143 us).
+// Forward (kWT): the tile is K-major, lane = weight row, and goes to tensor memory
+// (32 columns a unit; three steps fit beside the accumulators), by which the
+// shared-memory pipe is free to do the look-ups as shuffles: 105 us.  Input
+// gradient: the tile is MN-major, which only shared memory can hold, two steps of
+// it; with 64 tokens those would be 242 us against 217 (a step of 16 tokens in each
+// of 64 experts of 2048 x 1408).
 template <bool DX, int T>
 struct GroupGemmConfig {
     static constexpr int kBM = 128;                    // weight columns of one CTA
@@ -443,7 +445,7 @@ struct GroupGemmConfig {
     static constexpr int kDS = T > 256 ? 4 : T > 64 || kWT ? 3 : 2;  // slots of decoded tiles and of tokens
     static constexpr int kLC = T > 256 ? 8 : T > 64 ? 4 : 2 * kDS;   // slots of packed codes
     static constexpr int kWS = kWT ? 1 : kDS;          // slots of weight tiles in shared memory (kWT: extension only)
-    static constexpr int kBoxRows = kSubT / 2 < 32 ? kSubT / 2 : 32, kBoxes = kSubT / 2 / kBoxRows;
+    static constexpr int kBoxRows = T > 64 ? 32 : 16, kBoxes = kSubT / 2 / kBoxRows;
     static constexpr int kSub = kSubT / 2 * 128;       // a CTA's tokens of one accumulator, 64 deep
     static constexpr int kTok = kSubs * kSub;          // of all accumulators
     static constexpr int kCodes = kBM * 32, kW = kBM * 128;  // a packed and a decoded tile, 64 deep
