@@ -206,7 +206,7 @@ FusedPlan plan_fused(bool dx, int E, int64_t M, int64_t cols, int64_t contractio
         const int tile = few ? (dx ? 32 : 64) : rows <= 256 ? 256 : 512, wide = tile == 512 ? 64 : 128;
         const int k_main = static_cast<int>(div_up(contraction, wide)), k_ext = 2 * rank64(r) / wide;
         const double step = few           ? 1500.0
-                            : tile == 256 ? 1520.0 + 1.2 * size
+                            : tile == 256 ? (dx ? 1520.0 : 1400.0) + 1.2 * size
                                          : std::max(700.0 + 0.8 * size, 930.0);
         const double ends = few || tile == 256 ? 4000.0 : 3000.0 + 16.0 * size;
         // many tokens: only to put work on every SM at all

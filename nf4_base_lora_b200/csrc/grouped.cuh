@@ -420,9 +420,10 @@ struct RowMaps {
 // and with fewer than 350 tokens their issue, bound it.
 //
 // 256: the decode bounds it; steps of 128 by teams of eight warps (half the waits,
-// arrivals and turns of the copying and issuing warps per decoded weight) and two
-// sets of accumulators, so that MMAs run beside the epilogue.  125 tokens in each
-// of 64 experts of 2048 x 1408, a training step: 328 us against 345 with 512.
+// arrivals and turns of the copying and issuing warps per decoded weight).  Input
+// gradient: two sets of accumulators, so that MMAs run beside the epilogue; forward:
+// one, and the decoded tiles beside it in tensor memory (kWT, as below; 188 tokens
+// in each of eight experts of 4096 x 11008, a training step: 362 us against 384).
 //
 // 64 (forward), 32 (input gradient): two CTAs per SM of two teams each, whose
 // starts and ends overlap, and steps of 128 (two units per thread; steps of 64:
@@ -438,11 +439,11 @@ struct GroupGemmConfig {
     static constexpr int kBM = 128;                    // weight columns of one CTA
     static constexpr int kSubs = T > 256 ? 2 : 1;      // accumulators
     static constexpr int kSubT = T / kSubs;            // tokens of one, half of them per CTA
-    static constexpr bool kWT = T <= 64 && !DX;
+    static constexpr bool kWT = T <= 256 && !DX;  // decoded weights in tensor memory
     static constexpr int kTeams = T > 256 ? 4 : 2;
     static constexpr int kKS = T > 256 ? 1 : 2;        // 64s of the contraction in a step
     static constexpr int kUnits = T > 64 ? 1 : 2;      // (row, block) units of a step per thread
-    static constexpr int kDS = T > 256 ? 4 : T > 64 || kWT ? 3 : 2;  // slots of decoded tiles and of tokens
+    static constexpr int kDS = T > 256 || (T > 64 && kWT) ? 4 : T > 64 || kWT ? 3 : 2;  // slots of steps
     static constexpr int kLC = T > 256 ? 8 : T > 64 ? 4 : 2 * kDS;   // slots of packed codes
     static constexpr int kWS = kWT ? 1 : kDS;          // slots of weight tiles in shared memory (kWT: extension only)
     static constexpr int kBoxRows = T > 64 ? 32 : 16, kBoxes = kSubT / 2 / kBoxRows;
@@ -462,7 +463,7 @@ struct GroupGemmConfig {
     static constexpr int kMinBlocks = T > 64 ? 1 : 2;
     static constexpr int kAccs = T > 256 || kWT ? 1 : 2;       // accumulator sets: the next tile's MMAs run beside the epilogue
     static constexpr int kAccCols = T;                 // columns of a set
-    static constexpr int kTmemCols = kWT ? 256 : kAccs * T;
+    static constexpr int kTmemCols = kWT ? (T > 64 ? 512 : 256) : kAccs * T;
     static constexpr uint32_t kIdesc = make_idesc_bf16(2 * kBM, 0, DX ? 1 : 0, 0);  // without N
     // A wait for a barrier's phase is sound only where the phase before it is
     // known to be complete.  Code slots: a slot is always the same team's.  Decode
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     // Buffers: a step's slot ds, code slot cs, and its weight slot: ds, or with the
-    // decoded tiles in tensor memory the extension steps' own two
+    // decoded tiles in tensor memory the extension steps' own one
     auto t_buf = [&](int ds) { return base + ds * C::kTokBytes; };
     auto w_buf = [&](int ws) { return base + DS * C::kTokBytes + ws * C::kWBytes; };
     auto codes_buf = [&](int cs) { return base + DS * C::kTokBytes + C::kWS * C::kWBytes + cs * C::kCBytes; };
@@ -684,6 +685,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
         for (int i = 0; i < kAhead; ++i) codes_step();
         int ds = 0;             // slot of the tokens' step
         uint32_t done = 0;      // parity of the round over the slots
+        int since = DS;         // steps since the last extension step (kWT)
         bool stop = false;
         while (!stop && next_tile(wt, tt)) {
             const int n_iter = tt.n_main + tt.n_ext;
@@ -702,13 +704,18 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                 if (stop) break;
                 const bool main_step = is_main(tt, it);
                 const int j0 = (DROP ? it : it - tt.n_main) * C::kKS;  // of an extension step
-                if (C::kWT && !main_step && j0 >= C::kWS) {
-                    // the step that read this extension slot last, kWS before this one
-                    const int back = ds >= C::kWS ? ds - C::kWS : ds - C::kWS + DS;
-                    const uint32_t parity = ds >= C::kWS ? done : done ^ 1u;
-                    stop = __any_sync(0xFFFFFFFFu, !mbar_wait(&bar_done[back], parity, abort_flag));
-                    if (stop) break;
+                if (C::kWT && !main_step) {
+                    // the one slot of factors: free once the last extension step is
+                    // multiplied (DS or more steps back it is known to be)
+                    if (since < DS) {
+                        const int back = ds >= since ? ds - since : ds - since + DS;
+                        const uint32_t parity = ds >= since ? done : done ^ 1u;
+                        stop = __any_sync(0xFFFFFFFFu, !mbar_wait(&bar_done[back], parity, abort_flag));
+                        if (stop) break;
+                    }
+                    since = 0;
                 }
+                if (C::kWT) since = min(since + 1, DS);
                 if (elect_one()) {
                     if (rank == 0)
                         mbar_arrive_expect_tx(&bar_ready[ds], 2 * (bytes + (main_step ? 0 : C::kWBytes)));
@@ -735,7 +742,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                                 if (ms < tt.nsub)
                                     tma_load_2d_pair(t_buf(ds) + h * C::kTok + ms * C::kSub, &map_te.m[box[ms]], bar,
                                                      j * 64, sub_row(tt, ms));
-                            uint8_t* dst = w_buf(C::kWT ? j0 % C::kWS : ds) + h * C::kW;
+                            uint8_t* dst = w_buf(C::kWT ? 0 : ds) + h * C::kW;
                             if constexpr (DX) {
 #pragma unroll
                                 for (int c = 0; c < C::kBM / 64; ++c)
@@ -817,7 +824,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                             mma2_elect_ts(acc_d, wt + 8 * k, td + (k / 4) * (C::kTok / 16) + (k % 4) * kTk, idesc0,
                                           k > 0 ? 1u : acc);
                     } else {
-                        const int ws = C::kWT ? (it - n_main) % C::kWS : ds;
+                        const int ws = C::kWT ? 0 : ds;
                         const uint64_t wd = w_desc0 + static_cast<uint32_t>(ws) * (C::kWBytes / 16);
 #pragma unroll
                         for (int h = 0; h < C::kKS; ++h) {
@@ -1141,7 +1148,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
 #pragma unroll
                 for (int h = 0; h < C::kUnits; ++h)
                     decode_lane(codes_buf(cs) + h * C::kCodes + code_off, sc[h], level,
-                                tmem_d + lane_base + C::kAccs * C::kAccCols + (ds * C::kKS + h) * 32);
+                                tmem_d + lane_base + C::kAccs * C::kAccCols + (ds * C::kKS + h + half) * 32);
                 tmem_st_wait();
                 tc_fence_before();
             } else if (main_step) {
