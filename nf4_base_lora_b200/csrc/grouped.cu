@@ -154,13 +154,23 @@ Split split_steps(int64_t tiles, int64_t steps, int ctas) {
 int rank_width(int r) { return static_cast<int>(ceil_to(r, 16)); }
 int rank64(int r) { return static_cast<int>(ceil_to(r, 64)); }
 
+// Sets of accumulators that a CTA of T or V can hold beside another CTA's, and
+// the steps that one of them takes at most.
+int rank_sets(int r) { return 256 / rank_width(r); }
+constexpr int kRunSteps = 16;
+
 // Contraction splits of T (steps over K) and V (over N): two CTAs per SM.  A tile
 // for every SM is enough, though: halves would only add their sum (16000 tokens
 // over 64 experts of 2048 x 1408, step: 454 us with two parts, 438 with one).
-Split rows_split(int E, int64_t M, int64_t contraction, int num_sms) {
-    const int64_t tiles = likely_tiles(E, M, 128), steps = div_up(contraction, 64);
-    if (tiles >= num_sms) return {1, static_cast<int>(steps)};
-    return split_steps(tiles, steps, 2 * num_sms);
+Split rows_split(int E, int64_t M, int64_t contraction, int r, int num_sms) {
+    const int64_t tiles = likely_tiles(E, M, 128), steps = div_up(contraction, 64), most = kRunSteps * rank_sets(r);
+    Split s{1, static_cast<int>(steps)};
+    if (tiles < num_sms) s = split_steps(tiles, steps, 2 * num_sms);
+    if (s.per > most) {
+        const int64_t per = div_up(steps, div_up(steps, most));
+        s = {static_cast<int>(div_up(steps, per)), static_cast<int>(per)};
+    }
+    return s;
 }
 
 // Steps of a part of a group's rows for dB (out rows N) and dA (out rows K): so
@@ -242,9 +252,9 @@ Workspace layout(uint8_t* base, int64_t M, int E, int64_t N, int64_t K, int r, i
     w.T2 = reinterpret_cast<uint16_t*>(take(pair));
     if (backward) w.V2 = reinterpret_cast<uint16_t*>(take(pair));
     if (r % 8 != 0) w.B8 = reinterpret_cast<uint16_t*>(take(E * N * ceil_to(r, 8) * 2));
-    int64_t part = rows_split(E, M, K, num_sms).splits * M * rn;
+    int64_t part = rows_split(E, M, K, r, num_sms).splits * M * rn;
     if (backward) {
-        part = std::max(part, rows_split(E, M, N, num_sms).splits * M * rn);
+        part = std::max(part, rows_split(E, M, N, r, num_sms).splits * M * rn);
         part = std::max(part, most_partials(E, M, grad_part_steps(E, M, N, num_sms)) * N * rn);
         part = std::max(part, most_partials(E, M, grad_part_steps(E, M, K, num_sms)) * K * rn);
     }
@@ -288,7 +298,7 @@ cudaError_t launch_rank(const char* name, const CUtensorMap& a, const CUtensorMa
     int stages = std::min(kRankStages, 111 * 1024 / slot);
     if (stages < 2) stages = std::min(kRankStages, 224 * 1024 / slot);
     g.stages = stages;
-    const int cols = tok ? 2 * g.rn : g.rn;
+    const int sets = tok ? 2 : static_cast<int>(div_up(g.k_per_split, g.run_steps)), cols = sets * g.rn;
     g.tmem_cols = 32;
     while (g.tmem_cols < cols) g.tmem_cols *= 2;
     static bool done[64] = {};
@@ -315,10 +325,11 @@ RankArgs rank_args(const GroupCtx& c) {
 int rank_rows(const GroupCtx& c, bool is_t, const uint16_t* act, const uint16_t* factor, uint16_t* pair, float* out32,
               float* part) {
     const int64_t contraction = is_t ? c.K : c.N;
-    const Split sp = rows_split(c.E, c.M, contraction, c.num_sms);
+    const Split sp = rows_split(c.E, c.M, contraction, c.r, c.num_sms);
     RankArgs g = rank_args(c);
     g.k_steps = static_cast<int>(div_up(contraction, 64));
     g.k_per_split = sp.per;
+    g.run_steps = static_cast<int>(std::min<int64_t>(kRunSteps, std::max<int64_t>(4, div_up(sp.per, rank_sets(c.r)))));
     g.part = part;
     g.part_slice = c.M * g.rn;
     CUtensorMap ma, mb;

@@ -6,6 +6,11 @@
 //   RANK_DB  dB_e = sum_i dY_i^T T_i                   [N, r]
 //   RANK_DA  dA_e = gain sum_i V_i^T (keep_i .* X_i)   [r, K]
 //
+// T and V are sums over a whole layer's width that are kept in 32 bits, while the
+// tensor cores truncate at every addition: an accumulator takes 16 steps (1024
+// products) at most, then the next set of columns, and the sets are added rounded
+// (2048 wide: an error of 1e-6 of T's norm and not 2e-6).
+//
 // All four read one large activation once and are bound by that stream (HBM);
 // the MMAs are N = r wide and idle most of the time.  T and V split the
 // contraction over grid.z into fp32 partials that k_rank_rows_sum adds in a
@@ -49,6 +54,7 @@ struct RankArgs {
     int rows;          // dB: N, dA: K (output rows per expert)
     int k_steps;       // T, V: 64-wide steps of the contraction
     int k_per_split;   // T, V
+    int run_steps;     // T, V: steps into one set of accumulators
     int part_steps;    // dB, dA
     int slots;         // partials there is room for
     int r, rn;         // rank; MMA width, r rounded up to 16
@@ -297,8 +303,8 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
         constexpr uint32_t kAk = TOK ? 2048 / 16 : 32 / 16, kBk = MODE == RANK_T ? 32 / 16 : 2048 / 16;
         const uint64_t a0 = tile_desc(smem_u32(base), TOK, 0);
         const uint64_t b0 = tile_desc(smem_u32(base) + args.a_bytes, MODE != RANK_T, 0);
-        int slot = 0;
-        uint32_t phase = 0;
+        int slot = 0, run = 0;
+        uint32_t phase = 0, tmem_set = tmem_d;
         for (int it = 0; it < n_steps; ++it) {
             const bool last = own_bar(it);
             bool ok = mbar_wait(last ? &bar_last : &bar_full[slot], last ? 0u : phase, abort_flag);
@@ -310,9 +316,9 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
             const uint64_t bt = b0 + static_cast<uint32_t>(slot) * (slot_bytes / 16);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-                const uint32_t first = it * 4 + kk > 0 ? 1u : 0u;
+                const uint32_t first = run * 4 + kk > 0 ? 1u : 0u;
                 if constexpr (!TOK) {
-                    mma1_elect(tmem_d, at + kk * kAk, bt + kk * kBk, idesc, first);
+                    mma1_elect(tmem_set, at + kk * kAk, bt + kk * kBk, idesc, first);
                 } else {
                     const uint64_t hi = bt + kk * kBk, lo = hi + rchunks * (8192 / 16);
 #pragma unroll
@@ -323,6 +329,10 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
                 }
             }
             mma1_commit_elect(&bar_empty[slot]);
+            if (++run == args.run_steps && !TOK) {
+                run = 0;
+                tmem_set += args.rn;
+            }
             if (++slot == LS) {
                 slot = 0;
                 phase ^= 1u;
@@ -429,6 +439,18 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
                 if (n_steps > 0 && cc < args.rn) {
                     tmem_ld_32x32b_x8(at + cc, v);
                     tmem_ld_wait();
+                    if constexpr (!TOK) {
+                        uint32_t set = at + cc;
+                        for (int done = args.run_steps; done < n_steps; done += args.run_steps) {
+                            uint32_t x[8];
+                            set += args.rn;
+                            tmem_ld_32x32b_x8(set, x);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(x[j]));
+                        }
+                    }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = 0u;  // a group without rows; columns beyond r

@@ -216,3 +216,22 @@ def test_an_empty_batch(nf):
     assert Y.shape == (0, 64) and T.shape == (0, 8)
     _, dA, dB = nf.qlora_linear_dropout_bwd(w, d["A"], d["B"], 1.0, d["X"][:0], T, d["dY"][:0], 0.1, rng)
     assert not dA.any() and not dB.any()
+
+
+@pytest.mark.parametrize("M,r", [(300, 16), (19200, 16), (19200, 136)])
+def test_the_adapters_sum_keeps_32_bits(nf, M, r):
+    """T of a wide layer, few and many tiles, one set of accumulators and several.
+    A tensor-core addition truncates: at most one unit (2^-23) of the running sum,
+    half of one on average, and an accumulator takes at most 1024 products, 16 an
+    addition, so that T is off by about 64 2^-24 of its norm at most (688 additions
+    in a row would be 688 2^-24)."""
+    N, K = 64, 11008
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda")
+    w = nf.nf4_quantize(rn(N, K) * 0.02)
+    A, B, X = (rn(r, K) / r).bfloat16(), (rn(N, r) * 0.05).bfloat16(), rn(M, K).bfloat16()
+    _, T = nf.qlora_linear_dropout_fwd(w, A, B, 2.0, X, 0.0, None)
+    rows = torch.arange(0, M, max(1, M // 256), device="cuda")
+    ref = 2.0 * X[rows].double() @ A.double().T
+    err = (T[rows].double() - ref).norm() / ref.norm()
+    assert err <= 64 * 2.0 ** -24, float(err)
