@@ -366,9 +366,10 @@ int rank_rows(const GroupCtx& c, bool is_t, const uint16_t* act, const uint16_t*
                             s) == cudaSuccess ? 0 : -2;
 }
 
-// dB (act dY, pair T2) or dA (act X, pair V2).
+// dB (act dY, pair T2) or dA (act X, pair V2).  late_wait: the pair was complete
+// before the kernel launched last released its dependents.
 int rank_grad(const GroupCtx& c, bool is_b, const uint16_t* act, const uint16_t* pair, uint16_t* out, int accumulate,
-              float* part) {
+              bool late_wait, float* part) {
     const int64_t rows = is_b ? c.N : c.K;
     const int part_steps = grad_part_steps(c.E, c.M, rows, c.num_sms);
     const int64_t parts = most_parts(c.M, part_steps);
@@ -382,6 +383,7 @@ int rank_grad(const GroupCtx& c, bool is_b, const uint16_t* act, const uint16_t*
     g.part_slice = rows * g.rn;
     g.out = out;
     g.accumulate = accumulate;
+    g.late_wait = late_wait ? 1 : 0;
     CUtensorMap ma, mb;
     std::memset(&ma, 0, sizeof(ma));
     std::memset(&mb, 0, sizeof(mb));
@@ -551,24 +553,26 @@ int group_fwd(const GroupCtx& c, const uint16_t* A, const uint16_t* B, const uin
 int group_bwd(const GroupCtx& c, const uint16_t* A, const uint16_t* B, const uint16_t* X, const float* T_saved,
               const uint16_t* dY, uint16_t* dX, uint16_t* dA, uint16_t* dB, int accumulate, uint8_t* ws) {
     const Workspace w = layout(ws, c.M, c.E, c.N, c.K, c.r, c.num_sms, true);
+    const bool need_v = dX != nullptr || dA != nullptr, have_t = T_saved != nullptr;
     int rc = 0;
-    if (dX != nullptr || dA != nullptr) {
+    // The pair of T first: dB, which follows V or dX, then finds it complete and
+    // starts beside their last CTAs; dA finds V complete behind dX.
+    if (dB != nullptr && have_t) {
+        const int r64 = rank64(c.r);
+        if (launch_dependent("rank_pair", k_rank_pair, flat_grid(c.M * (r64 / 8), c.num_sms), 256, 0, c.stream, T_saved,
+                             c.M, c.r, r64, w.T2) != cudaSuccess)
+            rc = -2;
+    }
+    if (rc == 0 && need_v) {
         rc = padded_b(c, B, w.B8);
         if (rc == 0) rc = rank_rows(c, false, dY, B, w.V2, nullptr, w.part);
     }
     if (rc == 0 && dX != nullptr) rc = fused(c, true, dY, w.V2, A, w.fused_part, dX);
     if (rc == 0 && dB != nullptr) {
-        if (T_saved == nullptr) {
-            rc = rank_rows(c, true, X, A, w.T2, nullptr, w.part);
-        } else {
-            const int r64 = rank64(c.r);
-            if (launch_dependent("rank_pair", k_rank_pair, flat_grid(c.M * (r64 / 8), c.num_sms), 256, 0, c.stream, T_saved,
-                                 c.M, c.r, r64, w.T2) != cudaSuccess)
-                rc = -2;
-        }
-        if (rc == 0) rc = rank_grad(c, true, dY, w.T2, dB, accumulate, w.part);
+        if (!have_t) rc = rank_rows(c, true, X, A, w.T2, nullptr, w.part);
+        if (rc == 0) rc = rank_grad(c, true, dY, w.T2, dB, accumulate, have_t && need_v, w.part);
     }
-    if (rc == 0 && dA != nullptr) rc = rank_grad(c, false, X, w.V2, dA, accumulate, w.part);
+    if (rc == 0 && dA != nullptr) rc = rank_grad(c, false, X, w.V2, dA, accumulate, dX != nullptr, w.part);
     return rc;
 }
 

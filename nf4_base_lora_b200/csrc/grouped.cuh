@@ -503,10 +503,10 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the offsets, the activations and the encoded weight were complete before
     // the kernel this one depends on released it (that kernel waited for all
-    // earlier ones first); T2 / V2 is that kernel's and is waited for below
+    // earlier ones first); T2 / V2 is that kernel's and is waited for below, after
+    // which this one releases its own dependents
 
     // A tile of this pair.  Its steps: n_main of the contraction from kb0 on, and
     // in the first split the n_ext extension steps -- after them, or with dropout
@@ -732,7 +732,10 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                     } else {
                         // [hi | lo] against the factor twice
                         const int half = tt.n_ext * C::kKS / 2;
-                        if (!waited) grid_dependency_wait();
+                        if (!waited) {
+                            grid_dependency_wait();
+                            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+                        }
                         waited = true;
 #pragma unroll
                         for (int h = 0; h < C::kKS; ++h) {

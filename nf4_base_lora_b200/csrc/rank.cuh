@@ -68,6 +68,7 @@ struct RankArgs {
     int64_t part_slice;
     uint16_t* out;     // dB [E][N][r] / dA [E][r][K]
     int accumulate;
+    int late_wait;     // dB, dA: the inputs are complete at the start
     uint16_t* pair;    // T, V in one split: the pair [M, 2 r64] and (or NULL) fp32 [M, r], else partials
     float* out32;
 };
@@ -182,8 +183,11 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
     __shared__ int s_abort;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // it overwrites what the kernels before it may still read (the partials)
-    grid_dependency_wait();
+    // It overwrites what the kernels before it may still read (the partials).
+    // Where all that it reads was complete before the kernel this one depends on
+    // released it, only the results wait, and the products run beside that
+    // kernel's last CTAs.
+    if (!TOK || !args.late_wait) grid_dependency_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     GroupTile g;
@@ -194,8 +198,10 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
         step0 = blockIdx.z * args.k_per_split;
         n_steps = min(args.k_per_split, args.k_steps - step0);
     } else {
-        if (!find_part(args.offsets, args.E, args.M, args.part_steps, args.slots, blockIdx.y, lane, part))
+        if (!find_part(args.offsets, args.E, args.M, args.part_steps, args.slots, blockIdx.y, lane, part)) {
+            grid_dependency_wait();  // this grid's completion implies that of those before it
             return;
+        }
         g.e = part.e;
         begin = part.begin;
         g.row_end = part.end;
@@ -423,6 +429,7 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
         const int q = warp & 3, half = (ew >> 2) & 1;
         const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_accum, 0, abort_flag) && !*abort_flag);
         tc_fence_after();
+        if (TOK) grid_dependency_wait();
         if (ok && ew < 8) {
             // T, V: the two halves of the warps share the columns; dB, dA: they
             // take one accumulator each
@@ -647,8 +654,8 @@ __global__ void __launch_bounds__(256)
         slot0 += sl_all;
         __syncthreads();
     }
-    grid_dependency_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_dependency_wait();
     const int64_t slice = static_cast<int64_t>(rows) * rn;
     const int inner = (TRANSPOSED ? rows : r) / VEC, ld = TRANSPOSED ? rows : rn;
     const int64_t total = static_cast<int64_t>(rows) * r / VEC, chunks = (total + 255) / 256;
