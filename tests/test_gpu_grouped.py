@@ -141,6 +141,46 @@ def test_accumulation_recomputation_and_single_outputs(nf, counts):
                     + 1e-30).all()
 
 
+@pytest.mark.parametrize("E,N,K,r,counts,p", [
+    (3, 136, 192, 12, [300, 0, 129], 0.2), (3, 2048, 64, 8, [2000, 700, 1300], 0.1), (3, 64, 2048, 256, [600, 0, 300], 0.0),
+    (40, 72, 128, 8, [(7 * i) % 23 for i in range(40)], 0.1)])
+def test_results_do_not_depend_on_what_else_is_asked_for(nf, E, N, K, r, counts, p):
+    """Every choice of gradients, T saved or not, in one workspace that is
+    overwritten before each call, in eager calls and in a graph: the same bits."""
+    off, offsets = offsets_of(counts)
+    M = off[-1]
+    w, W, d = make(nf, E, N, K, r, M)
+    rng = rng_tensor((8, 9)) if p else None
+    ws = torch.empty(nf.qlora_grouped_bwd_workspace_bytes(M, E, N, K, r)
+                     + nf.qlora_grouped_fwd_workspace_bytes(M, E, N, K, r), dtype=torch.uint8, device="cuda")
+    out = [torch.empty_like(t) for t in (d["dY"], d["X"], d["A"], d["B"])] + [torch.empty(M, r, device="cuda")]
+
+    def call(save=True, **need):
+        for t in out:
+            t.fill_(7.0)
+        ws.fill_(255)
+        nf.qlora_grouped_fwd(w, d["A"], d["B"], 0.5, d["X"], offsets, p, rng, Y=out[0], T=out[4], workspace=ws)
+        nf.qlora_grouped_bwd(w, d["A"], d["B"], 0.5, d["X"], out[4] if save else None, d["dY"], offsets, p, rng,
+                             dX=out[1], dA=out[2], dB=out[3], workspace=ws, **need)
+    call()
+    first = [t.clone() for t in out]
+    for _ in range(4):
+        for save in (True, False):
+            for dx, da, db in ((1, 1, 1), (0, 1, 1), (1, 0, 1), (1, 1, 0), (0, 0, 1), (0, 1, 0), (1, 0, 0)):
+                call(save, need_dx=bool(dx), need_da=bool(da), need_db=bool(db))
+                for t, f, asked in zip(out, first, (1, dx, da, db, 1)):
+                    assert torch.equal(t, f) if asked else bool((t == 7.0).all())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+        call(False)
+        call()
+    for _ in range(10):
+        g.replay()
+        assert all(torch.equal(t, f) for t, f in zip(out, first))
+    nf.device_status()
+
+
 def test_a_graph_follows_offsets_that_change(nf):
     E, N, K, r, M = 4, 264, 320, 16, 300
     w, W, d = make(nf, E, N, K, r, M)
