@@ -398,10 +398,11 @@ int rank_grad(const GroupCtx& c, bool is_b, const uint16_t* act, const uint16_t*
     const bool vec = !is_b || c.r % 4 == 0;
     const int64_t sum_blocks = c.E * div_up(rows * c.r / (vec ? 4 : 1), 256);
     const dim3 sum_grid(static_cast<unsigned>(std::min<int64_t>(sum_blocks, 4 * c.num_sms)));
+    const int cap = std::max(1, std::min(c.E, g.slots / 2));
     auto sum = [&](auto kern) {
-        return launch_dependent("rank_grad_sum", kern, sum_grid, 256, 0, c.stream, c.offsets, c.E, g.M, part_steps,
-                                g.slots, static_cast<const float*>(part), static_cast<int>(rows), c.r, g.rn, g.alpha,
-                                out, accumulate);
+        return launch_dependent("rank_grad_sum", kern, sum_grid, 256, cap * kSumGroupBytes, c.stream, c.offsets, c.E,
+                                g.M, part_steps, g.slots, static_cast<const float*>(part), static_cast<int>(rows), c.r,
+                                g.rn, g.alpha, out, accumulate, cap);
     };
     return (!is_b ? sum(k_rank_grad_sum<true, 4>)
             : vec ? sum(k_rank_grad_sum<false, 4>)

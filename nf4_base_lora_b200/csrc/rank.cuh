@@ -600,15 +600,19 @@ __global__ void k_rank_pair(const float* __restrict__ src, int64_t M, int r, int
 // from partials [part][N][rn] or [part][rn][K], added in order.  Each block lists
 // those groups first and takes its share of their elements, so that the many
 // groups of one part cost nothing (a block per expert: 18 and 23 us for 64 experts
-// of 2048 x 1408, of which a few have several parts).  VEC elements at a time (4
-// needs r to be a multiple of 4 where not TRANSPOSED).
-constexpr int kSumExperts = 4096;
+// of 2048 x 1408, of which a few have several parts).  The list has room for `cap`
+// groups, which is min(E, slots / 2) and so all that valid offsets can make; it
+// lies in dynamic shared memory so that blocks fit beside the next kernel's.  VEC
+// elements at a time (4 needs r to be a multiple of 4 where not TRANSPOSED).
+constexpr int kSumGroupBytes = 10;
 template <bool TRANSPOSED, int VEC>
 __global__ void __launch_bounds__(256)
     k_rank_grad_sum(const int32_t* offsets, int E, int M, int part_steps, int slots, const float* __restrict__ part,
-                    int rows, int r, int rn, float alpha, uint16_t* __restrict__ out, int accumulate) {
-    __shared__ int s_slot[kSumExperts], s_parts[kSumExperts], s_warp[8][2];
-    __shared__ uint16_t s_e[kSumExperts];
+                    int rows, int r, int rn, float alpha, uint16_t* __restrict__ out, int accumulate, int cap) {
+    extern __shared__ int s_list[];
+    int *s_slot = s_list, *s_parts = s_list + cap;
+    uint16_t* s_e = reinterpret_cast<uint16_t*>(s_list + 2 * cap);
+    __shared__ int s_warp[8][2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // the offsets were complete before the kernels that this one follows
     int groups = 0, slot0 = 0;
@@ -643,17 +647,19 @@ __global__ void __launch_bounds__(256)
             g_all += s_warp[w][0];
             sl_all += s_warp[w][1];
         }
-        if (n > 1) {
-            s_e[groups + g - 1] = static_cast<uint16_t>(e);
-            s_slot[groups + g - 1] = slot0 + sl - taken;
+        const int k = groups + g - 1;
+        if (n > 1 && k < cap) {
+            s_e[k] = static_cast<uint16_t>(e);
+            s_slot[k] = slot0 + sl - taken;
             // what the slots do not hold was written as one part (offsets that
             // break their contract)
-            s_parts[groups + g - 1] = slot0 + sl <= slots ? n : 0;
+            s_parts[k] = slot0 + sl <= slots ? n : 0;
         }
         groups += g_all;
         slot0 += sl_all;
         __syncthreads();
     }
+    groups = min(groups, cap);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     grid_dependency_wait();
     const int64_t slice = static_cast<int64_t>(rows) * rn;

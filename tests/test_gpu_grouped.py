@@ -52,6 +52,7 @@ CASES = [
     (140, 72, 192, 8, [i % 4 for i in range(140)], 0, 3, 0.1, True),         # and 32-token ones
     (300, 64, 64, 8, [0] * 150 + [1200] + [1] * 148 + [700], 0, 0, 0.1, True),  # long groups far apart: summed parts
     (4096, 8, 64, 4, [1 if i % 3 else 0 for i in range(4096)], 0, 7, 0.0, True),  # most experts
+    (4096, 8, 64, 4, [0, 1152] * 2048, 0, 0, 0.0, True),                     # the longest list of groups with parts
     (2, 264, 192, 256, [600, 515], 0, 0, 0.25, True),                        # 512-token tiles, largest rank
     (2, 328, 448, 32, [505, 33], 1, 2, 0.0, False),                          # an odd number of blocks
 ]
