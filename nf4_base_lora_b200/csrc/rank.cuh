@@ -11,8 +11,11 @@
 // products) at most, then the next set of columns, and the sets are added rounded
 // (2048 wide: an error of 1e-6 of T's norm and not 2e-6).
 //
-// All four read one large activation once and are bound by that stream (HBM);
-// the MMAs are N = r wide and idle most of the time.  T and V split the
+// All four read one large activation once and are bound by that stream (HBM),
+// with dropout by the generator beside it; the MMAs are N = r wide and idle most of
+// the time.  8192 tokens over eight experts of 4096 -> 11008, r 16, dropout 0.05: V
+// 43 us and dB 42 us for 180 MB of dY (4.2 TB/s), T 23 us and dA 30 us for 67 MB of
+// X (2.9 and 2.2 TB/s).  T and V split the
 // contraction over grid.z into fp32 partials that k_rank_rows_sum adds in a
 // fixed order.  dB and dA contract over a group's rows, 256 output rows per CTA
 // (two accumulators sharing the narrow operand); a long group is cut into parts
@@ -260,7 +263,8 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
         uint32_t phase = 1;  // of the slot's release; passes at once in the first round
         bool stop = false;
         for (int it = 0; it < n_steps; ++it) {
-            stop = __any_sync(0xFFFFFFFFu, (it >= LS && !mbar_wait(&bar_empty[slot], phase, abort_flag)) || *abort_flag);
+            const bool late = it >= LS && !mbar_wait(&bar_empty[slot], phase, abort_flag);
+            stop = __any_sync(0xFFFFFFFFu, late || *abort_flag);
             if (stop) break;
             if (elect_one()) {
                 uint64_t* bar = own_bar(it) ? &bar_last : &bar_full[slot];
@@ -409,7 +413,8 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
                     const int chunks = kOutRows / 64 + 2 * rchunks, per = (64 - tail_rows) * 8;
                     for (int p = wt; p < chunks * per; p += kWork) {
                         const int chunk = p / per, rem = p - chunk * per;
-                        uint8_t* src = chunk < kOutRows / 64 ? a + chunk * 8192 : b_buf + (chunk - kOutRows / 64) * 8192;
+                        uint8_t* src =
+                            chunk < kOutRows / 64 ? a + chunk * 8192 : b_buf + (chunk - kOutRows / 64) * 8192;
                         *reinterpret_cast<uint4*>(src + tail_rows * 128 + rem * 16) = make_uint4(0, 0, 0, 0);
                     }
                 }
