@@ -301,6 +301,8 @@ cudaError_t launch_rank(const char* name, const CUtensorMap& a, const CUtensorMa
     const int sets = tok ? 2 : static_cast<int>(div_up(g.k_per_split, g.run_steps)), cols = sets * g.rn;
     g.tmem_cols = 32;
     while (g.tmem_cols < cols) g.tmem_cols *= 2;
+    // CTAs that share an SM must not wait for each other's tensor memory
+    if (g.tmem_cols > 256 && 2 * (stages * slot + 1024) <= 226 * 1024) return keep(cudaErrorInvalidConfiguration);
     static bool done[64] = {};
     const cudaError_t e = opt_in(reinterpret_cast<const void*>(&k_rank<MODE, DROP>), 226 * 1024, done);
     if (e != cudaSuccess) return keep(e);

@@ -189,7 +189,10 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
     // It overwrites what the kernels before it may still read (the partials).
     // Where all that it reads was complete before the kernel this one depends on
     // released it, only the results wait, and the products run beside that
-    // kernel's last CTAs.
+    // kernel's last CTAs.  Those have all started then, and none can be kept waiting
+    // by this kernel's tensor memory: what shares an SM with another CTA has 256
+    // columns at most (the input gradient's 32-token kernel 64), and what has more
+    // fills an SM's shared memory.
     if (!TOK || !args.late_wait) grid_dependency_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
