@@ -49,6 +49,7 @@
 #include "common.cuh"
 #include "decode.cuh"
 #include "nf4_levels.cuh"
+#include "rings.h"
 
 namespace nf4lora {
 
@@ -127,10 +128,8 @@ struct GemmConfig {
     static constexpr int kLSAuto = kLSRaw < kLSCap ? kLSRaw : kLSCap;
     static constexpr int kLS = LSTAGES > 0 ? LSTAGES : (kLSAuto > 8 ? 8 : kLSAuto);
     static_assert(kLS >= 2, "tile too large");
-    // The producer runs at most kLS k-steps ahead of the MMAs.  Its first
-    // parity wait on a decode slot (extension k-steps) is unambiguous only if
-    // it cannot be two phases ahead of that slot, i.e. kLS <= 2 * kDS.
-    static_assert(!kHasDec || kLS <= 2 * kDS, "load ring too deep for the decode ring");
+    // The producer's wait for a decode slot (extension k-steps): decode_slot_release.
+    static_assert(!kHasDec || kLS >= kDS, "load ring shallower than the decode ring");
     static_assert(kLoadA % 1024 == 0 && kLoadSlot % 1024 == 0 && kDecSlot % 1024 == 0, "swizzle alignment");
     static constexpr int kTeamThreads = kDecMN;               // one (row, block) unit each
     static constexpr int kTeamWarps = kTeamThreads / 32;
@@ -365,9 +364,10 @@ __global__ void __launch_bounds__(GemmConfig<BN, ASRC, BSRC, AE_MN, BE_MN, EPI, 
                 } else {
                     const int j = it - n_main;
                     // an extension tile on the decoded side lands in a decode slot
-                    if (C::kHasDec && it >= DS &&
-                        !mbar_wait(&bar_dempty[it % DS], ((it / DS) & 1u) ^ 1u, abort_flag))
-                        break;
+                    if (C::kHasDec && it >= DS) {
+                        const RingWait w = decode_slot_release(it, LS, DS);
+                        if (!mbar_wait(&bar_empty[w.slot], w.parity, abort_flag)) break;
+                    }
                     // the extension operand comes from the preceding kernel
                     if (j == 0 && args.pdl) grid_dependency_wait();
                     const int ja = args.ext_wrap_a > 0 ? j % args.ext_wrap_a : j;
