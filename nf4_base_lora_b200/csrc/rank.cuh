@@ -382,10 +382,13 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
                         grp = (static_cast<int64_t>(begin + k + row % 64) * args.drop_cols + out0 + 64 * (row / 64) +
                                8 * c) >> 3;
                     const int gcols = args.drop_cols >> 3;
+                    // rows of the tile that are the group's
+                    const int rows_kept = has_tail && it == n_steps - 1 ? tail_rows : 64;
 #pragma unroll
                     for (int i = 0; i < kPieces; ++i) {
                         int off;
                         uint64_t gi;
+                        bool inside = true;
                         if constexpr (!TOK) {
                             const int r = row + i * kRowStep;
                             off = r * 128 + ((c ^ (r & 7)) << 4);
@@ -397,25 +400,29 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
                             off = chunk * 8192 + rr * 128 + ((c ^ (rr & 7)) << 4);
                             gi = static_cast<uint64_t>(grp + 8 * (chunk - row / 64) +
                                                        static_cast<int64_t>(rr - row % 64) * gcols);
+                            inside = rr < rows_kept;
                         }
                         uint4* at = reinterpret_cast<uint4*>(a + off);
                         uint4 v = *at;
                         uint32_t m[4];
                         gen.masks(gi, m);
-                        v.x &= m[0];
-                        v.y &= m[1];
-                        v.z &= m[2];
-                        v.w &= m[3];
+                        v.x &= inside ? m[0] : 0u;
+                        v.y &= inside ? m[1] : 0u;
+                        v.z &= inside ? m[2] : 0u;
+                        v.w &= inside ? m[3] : 0u;
                         *at = v;
                     }
                 }
                 if (TOK && has_tail && it == n_steps - 1) {
-                    // rows behind the group's end: whole 128-byte rows of every chunk
-                    if (DROP) named_barrier_sync(4, kWork);  // the pieces above are other threads'
+                    // rows behind the group's end: whole 128-byte rows of every chunk;
+                    // with dropout the activation's are cleared with the pieces above, by
+                    // the threads that hold them, so that nobody waits for another warp
+                    // here (one whose wait ran out has left this loop)
+                    constexpr int kFirst = DROP ? kOutRows / 64 : 0;
                     uint8_t* b_buf = a + args.a_bytes;
-                    const int chunks = kOutRows / 64 + 2 * rchunks, per = (64 - tail_rows) * 8;
+                    const int chunks = kOutRows / 64 + 2 * rchunks - kFirst, per = (64 - tail_rows) * 8;
                     for (int p = wt; p < chunks * per; p += kWork) {
-                        const int chunk = p / per, rem = p - chunk * per;
+                        const int chunk = kFirst + p / per, rem = p % per;
                         uint8_t* src =
                             chunk < kOutRows / 64 ? a + chunk * 8192 : b_buf + (chunk - kOutRows / 64) * 8192;
                         *reinterpret_cast<uint4*>(src + tail_rows * 128 + rem * 16) = make_uint4(0, 0, 0, 0);

@@ -1,0 +1,48 @@
+"""Edges of the dropout and grouped layers that their kernels treat apart, on the
+GPU against 64-bit results."""
+import pytest
+import torch
+
+from adapter_ref import check, reference
+from test_gpu_dropout import rng_tensor
+from test_gpu_grouped import make, offsets_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def nf():
+    import nf4_base_lora_b200 as nf
+    return nf
+
+
+def compare(nf, E, N, K, r, counts, p, dq=True, first=0, behind=0, s=0.5, state=(3, 9)):
+    """Forward and backward against the 64-bit results; rows outside the groups
+    hold NaN and keep what the outputs had."""
+    off, offsets = offsets_of(counts, first)
+    M = off[-1] + behind
+    w, W, d = make(nf, E, N, K, r, M, dq)
+    rng = rng_tensor(state) if p else None
+    inside = slice(off[0], off[-1])
+    X, dY = torch.full_like(d["X"], float("nan")), torch.full_like(d["dY"], float("nan"))
+    X[inside], dY[inside] = d["X"][inside], d["dY"][inside]
+    Y, T, dX = torch.full_like(dY, 3.0), torch.full((M, r), 3.0, device="cuda"), torch.full_like(X, 3.0)
+    nf.qlora_grouped_fwd(w, d["A"], d["B"], s, X, offsets, p, rng, Y=Y, T=T)
+    _, dA, dB = nf.qlora_grouped_bwd(w, d["A"], d["B"], s, X, T, dY, offsets, p, rng, dX=dX)
+    torch.cuda.synchronize()
+    nf.device_status()
+    ref = reference(W, d["A"], d["B"], d["X"], d["dY"], off, s, p, state)
+    for name, got in (("T", T), ("Y", Y), ("dX", dX)):
+        check(got, ref, name, inside)
+        assert (got[:off[0]] == 3.0).all() and (got[off[-1]:] == 3.0).all(), name
+    check(dA, ref, "dA")
+    check(dB, ref, "dB")
+
+
+@pytest.mark.parametrize("p", [0.0, 0.25])
+@pytest.mark.parametrize("r", [8, 72])
+def test_a_group_may_end_on_any_row_of_a_step(nf, p, r):
+    """dA and dB contract over 64 rows a step; the rows behind a group's end are
+    the next group's, and NaN behind the last one."""
+    counts = [64 * (i % 4) + i for i in range(1, 64, 2)]
+    compare(nf, len(counts), 72, 320, r, counts, p, first=2, behind=61)

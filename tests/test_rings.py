@@ -28,3 +28,11 @@ def test_the_copying_thread_follows_the_rule():
     role = text[text.index("- producer"):text.index("TMEM + MMA issuer")]
     waits = re.findall(r"mbar_wait\(&(\w+)\[([^\]]*)\]", role)
     assert waits == [("bar_empty", "it % LS"), ("bar_empty", "w.slot")]
+
+
+def test_no_warp_waits_for_others_where_one_may_have_left():
+    """The clearing warps of the rank-r products leave their loop when a bounded
+    wait runs out; a barrier among them there would have no bound."""
+    text = open(os.path.join(CSRC, "rank.cuh")).read()
+    loop = text[text.index("- clearing"):text.index("- epilogue")]
+    assert not re.search(r"bar(rier)?\.sync|__syncthreads|named_barrier", loop)
