@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(GemmConfig<BN, ASRC, BSRC, AE_MN, BE_MN, EPI, 
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ TMEM + MMA issuer
+        __syncwarp();  // the barrier above does not bring a warp's threads together
         tmem_alloc(&s_tmem, C::kTmemCols);
         tmem_relinquish();
         tc_fence_before();
@@ -535,13 +536,15 @@ __global__ void __launch_bounds__(GemmConfig<BN, ASRC, BSRC, AE_MN, BE_MN, EPI, 
         const int part_idx = ew / 4;
         const int cw = BN / kColSplit;
         const int cbeg = part_idx * cw;
-        const bool ok = mbar_wait(&bar_accum, 0, abort_flag);
+        // tensor memory is read by whole warps: together, or (after a wait that ran out) not at all
+        const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_accum, 0, abort_flag) && !*abort_flag);
         tc_fence_after();
-        if constexpr (EPI != EPI_CLUSTER_BF16_T) if (ok && !*abort_flag) {
+        if constexpr (EPI != EPI_CLUSTER_BF16_T) if (ok) {
           for (int ms = 0; ms < MSUB; ++ms) {
             const int row = r0 + ms * C::kBM + q * 32 + lane;
             const bool row_ok = row < args.rows;
             for (int cc = cbeg; cc < cbeg + cw; cc += 32) {
+                __syncwarp();  // the lanes' stores differ
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(tmem_d + (static_cast<uint32_t>(q * 32) << 16) + ms * BN + cc, v);
                 tmem_ld_wait();
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(GemmConfig<BN, ASRC, BSRC, AE_MN, BE_MN, EPI, 
                 const uint32_t rank = cluster_ctarank();
                 const int splits = static_cast<int>(gridDim.z);
                 float* s_part = reinterpret_cast<float*>(base + LS * C::kLoadSlot + DS * C::kDecSlot);
-                const bool have = ok && !*abort_flag;
+                const bool have = ok;
                 // this CTA's partial: the used accumulators added in index order
                 float part[BN];
 #pragma unroll

@@ -775,6 +775,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ tensor memory, MMAs
+        __syncwarp();  // the cluster barrier does not bring a warp's threads together
         tmem2_alloc(&s_tmem, C::kTmemCols);
         tc_fence_before();
         asm volatile("bar.arrive 2, %0;" ::"r"(32 + kWork) : "memory");
@@ -1039,6 +1040,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             for (int ms = 0; ok && ms < t.nsub; ++ms) {
 #pragma unroll 1
                 for (int tt = tbeg; tt < tbeg + kShare && ms * C::kSubT + tt < t.tokens; tt += 32) {
+                    __syncwarp();  // the lanes' stores differ; tensor memory is read by the whole warp
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(tmem_d + lane_base + tl % C::kAccs * C::kAccCols + ms * C::kSubT + tt, v);
                     tmem_ld_wait();
@@ -1190,6 +1192,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
     cluster_arrive_release();
     cluster_wait_acquire();
     if (warp == 1) {
+        __syncwarp();
         tc_fence_after();
         tmem2_dealloc(s_tmem, C::kTmemCols);
     }

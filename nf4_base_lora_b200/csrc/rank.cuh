@@ -457,6 +457,7 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
             const uint32_t at = tmem_d + (static_cast<uint32_t>(q * 32) << 16) + (TOK ? half * args.rn : 0);
             const bool direct = part.parts == 1;
             for (int cc = cbeg; cc < cbeg + cols; cc += 8) {
+                __syncwarp();  // the lanes' stores differ; tensor memory is read by the whole warp
                 uint32_t v[8];
                 if (n_steps > 0 && cc < args.rn) {
                     tmem_ld_32x32b_x8(at + cc, v);

@@ -36,3 +36,19 @@ def test_no_warp_waits_for_others_where_one_may_have_left():
     text = open(os.path.join(CSRC, "rank.cuh")).read()
     loop = text[text.index("- clearing"):text.index("- epilogue")]
     assert not re.search(r"bar(rier)?\.sync|__syncthreads|named_barrier", loop)
+
+
+@pytest.mark.parametrize("name", ["rank.cuh", "grouped.cuh", "gemm.cuh"])
+def test_tensor_memory_is_read_by_converged_warps(name):
+    """A loop whose lanes store under conditions of their own brings the warp
+    together before it reads tensor memory again."""
+    text = open(os.path.join(CSRC, name)).read()
+    for m in re.finditer(r"for \(int (?:cc|tt) = \w+; [^\n]*\{\n(.*?)tmem_ld_32x32b", text, flags=re.S):
+        loop = text[m.start():]
+        depth, end = 0, 0
+        for end, c in enumerate(loop):
+            depth += (c == "{") - (c == "}")
+            if c == "}" and depth == 0:
+                break
+        if re.search(r"dst\[|\*reinterpret_cast<\w+\*>\(dst", loop[:end]):
+            assert "__syncwarp()" in m.group(1), m.group(0)
