@@ -434,6 +434,7 @@ cudaError_t launch_group_gemm(const char* name, FusedMaps& f, GroupGemmArgs g, b
     if (!*mapped) return cudaSuccess;
     const int64_t row_tiles = most_tiles(g.offsets, g.E, g.M, g.tile_rows);
     g.row_tiles = cols_fastest ? -1 : static_cast<int>(row_tiles);
+    g.most_row_tiles = static_cast<int>(row_tiles);
     // one CTA (or two) on every SM, each pair walking its share of the tiles
     const int64_t pairs =
         std::min<int64_t>(num_sms / 2 * C::kMinBlocks, row_tiles * g.col_tiles * g.splits);

@@ -395,6 +395,7 @@ struct GroupGemmArgs {
     int tile_rows;           // at most, a multiple of 32
     int col_tiles;
     int row_tiles;           // walked first when >= 0 (one dense group, its exact count), else the column tiles are
+    int most_row_tiles;      // that any division of the rows can need
     int walk_z, walk_fast, walk_slow;  // number of pairs = walk_z + splits (walk_fast + fast tiles walk_slow)
     // encoded weight: rows and blocks of one expert
     const int8_t* qscale;
@@ -547,7 +548,9 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             w.fast -= fast_n;
             ++w.slow;
         }
-        if (ct >= args.col_tiles) return false;
+        // offsets that break their rule may ask for more tiles than the rows can have
+        // (every group may be clamped to all rows): those are left out
+        if (ct >= args.col_tiles || rt >= args.most_row_tiles) return false;
         if (kept) {
             // the last group whose first tile is not beyond rt (groups without rows
             // share their first tile with the next one)
@@ -624,7 +627,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                 s_first[e] = tiles + incl - k;
                 s_size[e] = static_cast<uint16_t>(k > 0 ? ((n + k - 1) / k + 31) & ~31 : 0);
             }
-            tiles += __shfl_sync(0xFFFFFFFFu, incl, 31);
+            tiles = min(tiles + __shfl_sync(0xFFFFFFFFu, incl, 31), args.most_row_tiles);
         }
     }
     // both CTAs' barriers are initialised once this barrier is passed

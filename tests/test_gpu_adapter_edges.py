@@ -46,3 +46,36 @@ def test_a_group_may_end_on_any_row_of_a_step(nf, p, r):
     the next group's, and NaN behind the last one."""
     counts = [64 * (i % 4) + i for i in range(1, 64, 2)]
     compare(nf, len(counts), 72, 320, r, counts, p, first=2, behind=61)
+
+
+def elapsed_ms(f):
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    f()
+    a.record()
+    f()
+    b.record()
+    torch.cuda.synchronize()
+    return a.elapsed_time(b)
+
+
+@pytest.mark.parametrize("E", [100, 4096])
+def test_offsets_that_break_the_rule_ask_for_no_more_work(nf, E):
+    """Offsets that jump between 0 and M clamp every other group to all rows;
+    the call does no more than one division of the rows can need."""
+    M = 1 << 16
+    w, W, d = make(nf, E, 8, 64, 4, M)
+    out = {"Y": torch.empty_like(d["dY"]), "T": torch.empty((M, 4), device="cuda")}
+    good = torch.linspace(0, M, E + 1, device="cuda").to(torch.int32)
+    bad = (torch.arange(E + 1, device="cuda") % 2 * M).to(torch.int32)
+    ws = torch.empty(nf.qlora_grouped_bwd_workspace_bytes(M, E, 8, 64, 4), dtype=torch.uint8, device="cuda")
+
+    def call(offsets):
+        nf.qlora_grouped_fwd(w, d["A"], d["B"], 1.0, d["X"], offsets, workspace=ws, **out)
+        nf.qlora_grouped_bwd(w, d["A"], d["B"], 1.0, d["X"], out["T"], d["dY"], offsets, workspace=ws)
+    t_good = elapsed_ms(lambda: call(good))
+    nf.device_status()
+    t_bad = elapsed_ms(lambda: call(bad))
+    with pytest.raises(nf.Nf4Error, match="offsets"):
+        nf.device_status()
+    # E / 2 times the rows if every group were run
+    assert t_bad <= 8 * t_good + 1.0, (t_bad, t_good)
