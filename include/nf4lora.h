@@ -325,7 +325,9 @@ int qlora_linear_dropout_bwd(const nf4_tensor* w, const uint16_t* A, const uint1
  * [M, d_in].  Nothing is copied to the host: the grid covers the most row
  * tiles that M rows in n_experts groups can need.
  * Offsets that break the rule lead no access out of the arrays; the results
- * are then undefined, and nf4lora_device_status() returns NF4_ERR_INVALID_ARG.
+ * are then undefined, and nf4lora_device_status() returns NF4_ERR_INVALID_ARG
+ * (a call that has nothing to compute -- M = 0, or no output asked for -- does
+ * not read them).
  * Requirements: 1 <= n_experts <= NF4_MAX_EXPERTS, d_out % 8 == 0,
  * n_experts * d_out * d_in / 64 < 2^32; no output overlaps an input or another
  * output; else as for

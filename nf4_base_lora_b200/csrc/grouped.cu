@@ -329,6 +329,7 @@ int rank_rows(const GroupCtx& c, bool is_t, const uint16_t* act, const uint16_t*
     const int64_t contraction = is_t ? c.K : c.N;
     const Split sp = rows_split(c.E, c.M, contraction, c.r, c.num_sms);
     RankArgs g = rank_args(c);
+    g.check = c.offsets != nullptr ? 1 : 0;
     g.k_steps = static_cast<int>(div_up(contraction, 64));
     g.k_per_split = sp.per;
     g.run_steps = static_cast<int>(std::min<int64_t>(kRunSteps, std::max<int64_t>(4, div_up(sp.per, rank_sets(c.r)))));
@@ -369,14 +370,16 @@ int rank_rows(const GroupCtx& c, bool is_t, const uint16_t* act, const uint16_t*
 }
 
 // dB (act dY, pair T2) or dA (act X, pair V2).  late_wait: the pair was complete
-// before the kernel launched last released its dependents.
+// before the kernel launched last released its dependents.  check: no T or V kernel
+// of this call has looked at the offsets.
 int rank_grad(const GroupCtx& c, bool is_b, const uint16_t* act, const uint16_t* pair, uint16_t* out, int accumulate,
-              bool late_wait, float* part) {
+              bool late_wait, bool check, float* part) {
     const int64_t rows = is_b ? c.N : c.K;
     const int part_steps = grad_part_steps(c.E, c.M, rows, c.num_sms);
     const int64_t parts = most_parts(c.M, part_steps);
     const bool drop = !is_b && c.drop.threshold != 0;
     RankArgs g = rank_args(c);
+    g.check = check && c.offsets != nullptr ? 1 : 0;
     g.rows = static_cast<int>(rows);
     g.part_steps = part_steps;
     g.slots = static_cast<int>(most_partials(c.E, c.M, part_steps));
@@ -574,9 +577,9 @@ int group_bwd(const GroupCtx& c, const uint16_t* A, const uint16_t* B, const uin
     if (rc == 0 && dX != nullptr) rc = fused(c, true, dY, w.V2, A, w.fused_part, dX);
     if (rc == 0 && dB != nullptr) {
         if (!have_t) rc = rank_rows(c, true, X, A, w.T2, nullptr, w.part);
-        if (rc == 0) rc = rank_grad(c, true, dY, w.T2, dB, accumulate, have_t && need_v, w.part);
+        if (rc == 0) rc = rank_grad(c, true, dY, w.T2, dB, accumulate, have_t && need_v, have_t && !need_v, w.part);
     }
-    if (rc == 0 && dA != nullptr) rc = rank_grad(c, false, X, w.V2, dA, accumulate, dX != nullptr, w.part);
+    if (rc == 0 && dA != nullptr) rc = rank_grad(c, false, X, w.V2, dA, accumulate, dX != nullptr, false, w.part);
     return rc;
 }
 

@@ -52,6 +52,7 @@ enum RankMode : int { RANK_T = 0, RANK_V = 1, RANK_DB = 2, RANK_DA = 3 };
 
 struct RankArgs {
     const int32_t* offsets;
+    int check;         // the first kernel of a call that reads the offsets: looks whether they keep their rule
     int E;
     int M;
     int rows;          // dB: N, dA: K (output rows per expert)
@@ -196,6 +197,17 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
     if (!TOK || !args.late_wait) grid_dependency_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+    if (args.check && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+        // offsets that break the contract are reported in the device status word,
+        // also where they leave this block, or every block, without rows
+        bool bad = false;
+        for (int e = threadIdx.x; e <= args.E; e += C::kThreads) {
+            const int v = __ldcg(args.offsets + e);
+            bad |= v < (e > 0 ? max(0, __ldcg(args.offsets + e - 1)) : 0) || v > args.M;
+        }
+        if (bad) atomicCAS(&g_device_status, 0, kStatusOffsets);
+        __syncwarp();
+    }
     GroupTile g;
     int out0 = 0, begin = 0, n_steps, step0;
     RankPart part{0, 0, 0, 1, 0, 0};
@@ -218,15 +230,6 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
         n_steps = max(0, min(per, total - step0));
     }
     n_steps = __shfl_sync(0xFFFFFFFFu, n_steps, 0);  // said to be uniform, as what follows from it
-    if (!TOK && args.offsets != nullptr && blockIdx.x == 0 && blockIdx.z == 0) {
-        // offsets that break the contract are reported in the device status word
-        bool bad = false;
-        for (int e = threadIdx.x; e <= args.E; e += C::kThreads) {
-            const int v = __ldcg(args.offsets + e);
-            bad |= v < (e > 0 ? max(0, __ldcg(args.offsets + e - 1)) : 0) || v > args.M;
-        }
-        if (bad) atomicCAS(&g_device_status, 0, kStatusOffsets);
-    }
     const int LS = args.stages, slot_bytes = args.a_bytes + args.b_bytes;
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);

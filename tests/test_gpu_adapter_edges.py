@@ -79,3 +79,28 @@ def test_offsets_that_break_the_rule_ask_for_no_more_work(nf, E):
         nf.device_status()
     # E / 2 times the rows if every group were run
     assert t_bad <= 8 * t_good + 1.0, (t_bad, t_good)
+
+
+# none of these leaves a group a row, or only the last one
+NO_ROWS = ([64, 40, 20, 0], [-1] * 4, [65] * 4, [64, 64, 64, 65], [-5, -3, -1, 0], [1 << 30] * 4)
+
+
+@pytest.mark.parametrize("off", [*NO_ROWS, [0, 40, 20, 64]], ids=str)
+def test_every_call_reports_offsets_that_break_the_rule(nf, off):
+    """Whatever the call asks for, and also where the clamped groups have no rows
+    so that no kernel has work."""
+    E, N, K, r, M = 3, 128, 128, 8, 64
+    w, W, d = make(nf, E, N, K, r, M)
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    T = torch.zeros((M, r), device="cuda")
+
+    def reported(f):
+        f()
+        with pytest.raises(nf.Nf4Error, match="offsets"):
+            nf.device_status()
+        nf.device_status()
+    reported(lambda: nf.qlora_grouped_fwd(w, d["A"], d["B"], 1.0, d["X"], offsets))
+    for dx, da, db in ((1, 1, 1), (1, 0, 0), (0, 1, 0), (0, 0, 1), (0, 1, 1), (1, 0, 1)):
+        for saved in (T, None):
+            reported(lambda: nf.qlora_grouped_bwd(w, d["A"], d["B"], 1.0, d["X"], saved, d["dY"], offsets,
+                                                  need_dx=bool(dx), need_da=bool(da), need_db=bool(db)))
