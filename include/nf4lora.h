@@ -289,7 +289,12 @@ int lora_dropout(const void* X, int64_t n, int dtype, const lora_dropout_params*
  * D is never formed in memory.  dropout NULL or p = 0 is the plain layer (its
  * own kernels: results agree with qlora_linear_fwd / _bwd to rounding, not bit
  * for bit).  A value that is dropped cannot reach T or dA, nor V A reach a
- * dropped element of dX, even if it is a NaN or infinite.  Everything else as
+ * dropped element of dX, even if it is a NaN or infinite.  T and V enter the
+ * later products as pairs of bfloat16 values, high + low (off by 2^-16 of the
+ * value at most); infinite ones give the formula's infinities.  An infinite
+ * element of what such a pair is multiplied by (B in Y, A in dX, X in dA, dY in
+ * dB) may give NaN where the formula gives an infinity: the low half may be zero
+ * or of the other sign.  Everything else as
  * for qlora_linear_fwd / _bwd: shapes, T_saved, NULL outputs,
  * accumulate_grads, M = 0; ws >= the sizes below.
  */

@@ -324,6 +324,17 @@ __device__ __forceinline__ float bf16_bits_to_float(uint16_t b) {
     return __uint_as_float(static_cast<uint32_t>(b) << 16);
 }
 
+// The high half of the pair by which an fp32 value enters a product of bf16
+// operands: v rounded to bf16; the low half is v minus it, rounded too (together
+// off by 2^-16 v at most).  The high half stays in bf16's finite range, so that
+// the low half of a finite value near the end of fp32's is its true difference,
+// and that of an infinite value is that infinity: the halves' products then have
+// one sign, where an infinite high half would leave inf - inf for the low one.
+__device__ __forceinline__ float bf16_high_part(float v) {
+    constexpr float kMax = 3.3895313892515355e38f;  // 2^128 - 2^120
+    return __bfloat162float(__float2bfloat16_rn(fminf(fmaxf(v, -kMax), kMax)));
+}
+
 }  // namespace nf4lora
 
 namespace nf4lora {

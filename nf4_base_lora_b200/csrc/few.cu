@@ -40,8 +40,8 @@ __device__ __forceinline__ void prefetch_l2_pieces(const void* src, uint32_t byt
 }
 
 __device__ __forceinline__ void store_split(uint16_t* dst_hi, uint16_t* dst_lo, float v) {
-    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-    const __nv_bfloat16 lo = __float2bfloat16_rn(v - __bfloat162float(hi));
+    const float high = bf16_high_part(v);
+    const __nv_bfloat16 hi = __float2bfloat16_rn(high), lo = __float2bfloat16_rn(v - high);
     *dst_hi = *reinterpret_cast<const uint16_t*>(&hi);
     *dst_lo = *reinterpret_cast<const uint16_t*>(&lo);
 }

@@ -180,8 +180,8 @@ __global__ void k_reduce_splits(const ReduceArgs a) {
         const float v = acc * a.alpha;
         uint16_t* o = a.out + r * a.ldo + c;
         if (a.lo_off > 0) {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-            const __nv_bfloat16 lo = __float2bfloat16_rn(v - __bfloat162float(hi));
+            const float high = bf16_high_part(v);
+            const __nv_bfloat16 hi = __float2bfloat16_rn(high), lo = __float2bfloat16_rn(v - high);
             o[0] = *reinterpret_cast<const uint16_t*>(&hi);
             o[a.lo_off] = *reinterpret_cast<const uint16_t*>(&lo);
         } else {
@@ -238,8 +238,8 @@ __global__ void k_split_from_f32(const float* __restrict__ src, int64_t M, int r
         const int64_t m = i / r64;
         const int j = static_cast<int>(i % r64);
         const float v = j < r ? src[m * r + j] : 0.0f;
-        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-        const __nv_bfloat16 lo = __float2bfloat16_rn(v - __bfloat162float(hi));
+        const float high = bf16_high_part(v);
+        const __nv_bfloat16 hi = __float2bfloat16_rn(high), lo = __float2bfloat16_rn(v - high);
         dst[m * 2 * r64 + j] = *reinterpret_cast<const uint16_t*>(&hi);
         dst[m * 2 * r64 + r64 + j] = *reinterpret_cast<const uint16_t*>(&lo);
     }

@@ -85,7 +85,7 @@ __device__ __forceinline__ void store_pair(float (&v)[8], int64_t row, int j, in
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
         if (j + u >= r) v[u] = 0.0f;
-        hi[u] = __bfloat162float(__float2bfloat16_rn(v[u]));
+        hi[u] = bf16_high_part(v[u]);
         lo[u] = v[u] - hi[u];
         if (out32 != nullptr && j + u < r) out32[row * r + j + u] = v[u];
     }

@@ -104,3 +104,88 @@ def test_every_call_reports_offsets_that_break_the_rule(nf, off):
         for saved in (T, None):
             reported(lambda: nf.qlora_grouped_bwd(w, d["A"], d["B"], 1.0, d["X"], saved, d["dY"], offsets,
                                                   need_dx=bool(dx), need_da=bool(da), need_db=bool(db)))
+
+
+def signed(g, rows, cols):
+    """|normal| with one sign a column, so that sums over rows of infinities have one."""
+    sign = torch.where(torch.rand(cols, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    return ((torch.randn(rows, cols, generator=g, device="cuda").abs() + 0.01) * sign).bfloat16()
+
+
+def layer_calls(nf, kind, w, A, B, s, X, dY, T=None):
+    """(Y, T, dX, dA, dB) of the plain, the dropout (p = 0) or the grouped layer;
+    T: what the backward gets, else the forward's."""
+    if kind == "plain":
+        Y, T0 = nf.qlora_linear_fwd(w, A, B, s, X)
+        return (Y, T0, *nf.qlora_linear_bwd(w, A, B, s, X, T0 if T is None else T, dY))
+    if kind == "dropout":
+        Y, T0 = nf.qlora_linear_dropout_fwd(w, A, B, s, X, 0.0, None)
+        return (Y, T0, *nf.qlora_linear_dropout_bwd(w, A, B, s, X, T0 if T is None else T, dY, 0.0, None))
+    offsets = torch.tensor([0, X.shape[0]], dtype=torch.int32, device="cuda")
+    Y, T0 = nf.qlora_grouped_fwd(w, A[None], B[None], s, X, offsets)
+    dX, dA, dB = nf.qlora_grouped_bwd(w, A[None], B[None], s, X, T0 if T is None else T, dY, offsets)
+    return Y, T0, dX, dA[0], dB[0]
+
+
+def same_or_close(got, ref, name):
+    """NaN and infinities exactly; finite elements to 2^-6 of the largest (a rounding is 2^-8)."""
+    got, fin = got.double(), torch.isfinite(ref)
+    assert torch.equal(torch.isnan(got), torch.isnan(ref)), name
+    assert torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)]), name
+    assert ((got - ref).abs()[fin] <= 2.0 ** -6 * ref.abs()[fin].max()).all() if fin.any() else True, name
+
+
+@pytest.mark.parametrize("M", [1, 5, 200])
+@pytest.mark.parametrize("kind", ["plain", "dropout", "grouped"])
+def test_an_infinite_t_or_v_gives_the_formulas_infinities(nf, kind, M):
+    """T and V enter the products as pairs of 16-bit values; an infinite one, from
+    an infinite element of A or B, is the formula's signed infinity in all that
+    follows from it, never a NaN."""
+    N, K, r, s = 136, 192, 8, 0.5
+    g = torch.Generator(device="cuda").manual_seed(M)
+    w = nf.nf4_quantize(torch.randn(N, K, generator=g, device="cuda") * 0.02)
+    W = nf.nf4_dequantize(w).double()
+    X, dY = signed(g, M, K), signed(g, M, N)
+    A, B = signed(g, K, r).t().contiguous(), signed(g, N, r)
+    for which in "AB":
+        a, b = A.clone(), B.clone()
+        (a if which == "A" else b)[(3, 70) if which == "A" else (70, 3)] = float("inf")
+        Y, T, dX, dA, dB = layer_calls(nf, kind, w, a, b, s, X, dY)
+        x, dy, ad, bd = X.double(), dY.double(), a.double(), b.double()
+        if which == "A":
+            t = s * (x @ ad.T)
+            same_or_close(T, t, "T")
+            same_or_close(Y, x @ W.T + t @ bd.T, "Y")
+            same_or_close(dB, dy.T @ t, "dB")
+        else:
+            v = s * (dy @ bd)
+            same_or_close(dX, dy @ W + v @ ad, "dX")
+            same_or_close(dA, v.T @ x, "dA")
+        torch.cuda.synchronize()
+    nf.device_status()
+
+
+@pytest.mark.parametrize("M", [1, 5, 200])
+@pytest.mark.parametrize("kind", ["plain", "dropout", "grouped"])
+def test_a_t_or_v_beyond_the_16_bit_range_is_exact(nf, kind, M):
+    """2^128 - 2^118 is a finite fp32 value that rounds to infinity in 16 bits.
+    Its products with factors of about 2^-100 are finite: within the roundings
+    (2^-8 of the result and what the pair leaves, 2^-16)."""
+    N, K, r = 136, 192, 8
+    big, tiny = 2.0 ** 127, 2.0 ** -100
+    g = torch.Generator(device="cuda").manual_seed(7)
+    w = nf.nf4_quantize(torch.zeros(N, K, device="cuda"))
+    X, dY = torch.zeros(M, K, device="cuda"), torch.zeros(M, N, device="cuda")
+    A, B = torch.full((r, K), tiny, device="cuda"), torch.full((N, r), tiny, device="cuda")
+    # T[:, 3] = V[:, 3] = 255 / 128 2^127 + 1.5 2^119
+    for act, fac in ((X, A[3]), (dY, B[:, 3])):
+        act[:, 0], act[:, 1] = 255 / 128, 1.5
+        fac[0], fac[1] = big, 2.0 ** 119
+    Y, T, dX, dA, dB = layer_calls(nf, kind, w, *(t.bfloat16() for t in (A, B)), 1.0, X.bfloat16(), dY.bfloat16())
+    x, dy, a, b = X.double(), dY.double(), A.double(), B.double()
+    t, v = x @ a.T, dy @ b
+    assert torch.equal(T.double(), t.float().double()) and float(t[0, 3]) == 2.0 ** 128 - 2.0 ** 118
+    for name, got, ref in (("Y", Y, t @ b.T), ("dX", dX, v @ a), ("dA", dA, v.T @ x), ("dB", dB, dy.T @ t)):
+        # columns and rows that meet the large elements twice are infinite in 32 bits already
+        fin = ref.abs() < 2.0 ** 120
+        assert fin.any() and ((got.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -14) * ref.abs())[fin].all(), name
