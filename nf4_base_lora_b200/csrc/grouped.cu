@@ -174,11 +174,17 @@ Split rows_split(int E, int64_t M, int64_t contraction, int r, int num_sms) {
 }
 
 // Steps of a part of a group's rows for dB (out rows N) and dA (out rows K): so
-// many that the parts of an even batch are about one per SM, at least eight.
+// many that the parts of an even batch are about one per SM, at least eight and at
+// most kGradSteps, a part having one accumulator of additions that truncate (sums
+// of one sign over 262144 rows of 11008 columns come out 6.2e-4 too small on
+// average in three parts, 3.2e-5 in 32; half a unit of the 16-bit result is 2e-3 to
+// 4e-3).  The number of parts stays one that a grid can have.
+constexpr int64_t kGradSteps = 128, kMostParts = 1 << 14;
 int grad_part_steps(int E, int64_t M, int64_t out_rows, int num_sms) {
     const int64_t groups = std::min<int64_t>(E, M), steps = div_up(div_up(M, groups), 64);
     const int64_t parts = std::max<int64_t>(1, num_sms / (div_up(out_rows, 256) * groups));
-    return static_cast<int>(std::max<int64_t>(8, div_up(steps, parts)));
+    const int64_t per = std::min(std::max<int64_t>(8, div_up(steps, parts)), kGradSteps);
+    return static_cast<int>(std::max(per, div_up(div_up(M, 64), kMostParts)));
 }
 // Parts of the longest group there can be, and partials in all: a group of n > p
 // steps has at most 2 n / p parts.

@@ -21,7 +21,8 @@
 // (two accumulators sharing the narrow operand); a long group is cut into parts
 // of at most part_steps steps, whose partials k_rank_grad_sum adds in order,
 // while a group of one part writes its result itself -- so a skewed batch does
-// not wait for its longest group, and short groups cost no partials.  T and V
+// not wait for its longest group, short groups cost no partials, and no
+// accumulator takes more than 128 steps of truncating additions.  T and V
 // enter dB and dA as their 16-bit pair [hi | lo], both halves into the same
 // accumulator columns.
 //

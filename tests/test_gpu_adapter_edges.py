@@ -189,3 +189,39 @@ def test_a_t_or_v_beyond_the_16_bit_range_is_exact(nf, kind, M):
         # columns and rows that meet the large elements twice are infinite in 32 bits already
         fin = ref.abs() < 2.0 ** 120
         assert fin.any() and ((got.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -14) * ref.abs())[fin].all(), name
+
+
+@pytest.mark.parametrize("which", ["dB", "dA"])
+def test_gradients_over_many_rows_keep_their_precision(nf, which):
+    """Tensor-core additions truncate, so a long sum of one sign is too small by up
+    to a unit (2^-23) of the running sum an addition, half a unit on average, of a
+    running sum that is half the result on average.  A row of 64 takes 8 additions
+    (two halves of the pair, 16 rows each) and an accumulator 128 rows of 64 at
+    most: 1024 2^-25 on average, however many rows there are.  To see more of the
+    sum than the 8 bits of a gradient, it is accumulated onto the negative result
+    rounded to them, which the kernels do in 32 bits: what comes out is at most 2^-8
+    of the result, and rounded to 2^-8 of that."""
+    M, r, wide, narrow = 1 << 18, 8, 11008, 64
+    N, K = (wide, narrow) if which == "dB" else (narrow, wide)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = nf.nf4_quantize(torch.randn(N, K, generator=g, device="cuda") * 0.02)
+    pos = lambda *s: torch.rand(s, generator=g, device="cuda") + 0.5
+    A, B = pos(r, K).bfloat16(), pos(N, r).bfloat16()
+    act = torch.empty((M, wide), dtype=torch.bfloat16, device="cuda")
+    for i in range(0, M, 1 << 14):
+        act[i:i + (1 << 14)] = pos(1 << 14, wide)
+    other = pos(M, narrow).bfloat16()
+    X, dY = (other, act) if which == "dB" else (act, other)
+    T = pos(M, r)
+    f = T if which == "dB" else dY.double() @ B.double()
+    ref = torch.zeros((r, wide), dtype=torch.float64, device="cuda")
+    for i in range(0, M, 1 << 14):
+        ref += f[i:i + (1 << 14)].double().T @ act[i:i + (1 << 14)].double()
+    grad = -(ref.t() if which == "dB" else ref).bfloat16().contiguous()
+    before = grad.double()
+    out = {"dA": grad} if which == "dA" else {"dB": grad}
+    nf.qlora_linear_dropout_bwd(w, A, B, 1.0, X, T, dY, 0.0, None, need_dx=False, need_da=which == "dA",
+                                need_db=which == "dB", accumulate=True, **out)
+    got = grad.double() - before
+    mean = (((got.t() if which == "dB" else got) - ref) / ref).mean()
+    assert abs(float(mean)) <= 1024 * 2.0 ** -25 + 2.0 ** -16, float(mean)
