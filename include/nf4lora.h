@@ -275,8 +275,8 @@ typedef struct {
  * (bfloat16 as uint16_t, or float): computed in fp32, rounded once; a dropped
  * element is 0 whatever X held.  The gradient is the same call on the incoming
  * gradient.  Element i of an [M, d_in] array here is element i of X in the
- * layer calls below: the same state gives the same mask.  out may be X.
- * n = 0 does nothing.
+ * layer calls below: the same state gives the same mask.  out may be X, but not
+ * overlap it otherwise.  n = 0 does nothing.
  */
 int lora_dropout(const void* X, int64_t n, int dtype, const lora_dropout_params* dropout, void* out, void* stream);
 

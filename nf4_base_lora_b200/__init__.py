@@ -380,7 +380,7 @@ def lora_dropout(X: torch.Tensor, p: float, rng: Optional[torch.Tensor],
     no mask is stored: the keep decisions are a function of rng = (seed,
     offset), a CUDA int64 tensor, and the element's index (lora_dropout_params
     in include/nf4lora.h).  The gradient is the same call on the incoming
-    gradient.  `out` may be X."""
+    gradient.  `out` may be X, but not overlap it otherwise."""
     dt, dev = X.dtype, X.device
     if (dt is not _BF16 and dt is not _F32) or dev.type != "cuda" or not X.is_contiguous():
         raise ValueError("X must be a contiguous bfloat16 or float32 CUDA tensor")

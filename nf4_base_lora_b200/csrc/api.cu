@@ -319,6 +319,10 @@ int lora_dropout(const void* X, int64_t n, int dtype, const lora_dropout_params*
     if (n == 0) return ok();
     if (!X || !out) return fail(NF4_ERR_INVALID_ARG, "X or out is NULL");
     if (!aligned16(X) || !aligned16(out)) return fail(NF4_ERR_MISALIGNED, "X or out not 16-byte aligned");
+    const size_t bytes = static_cast<size_t>(n) * (dtype == NF4_DTYPE_BF16 ? 2 : 4);
+    const uintptr_t in0 = reinterpret_cast<uintptr_t>(X), out0 = reinterpret_cast<uintptr_t>(out);
+    if (in0 != out0 && (in0 < out0 ? out0 - in0 : in0 - out0) < bytes)
+        return fail(NF4_ERR_INVALID_ARG, "out overlaps X without being X");
     int sms = 0;
     rc = check_device(&sms);
     if (rc) return rc;
@@ -327,7 +331,6 @@ int lora_dropout(const void* X, int64_t n, int dtype, const lora_dropout_params*
     if (drop.threshold != 0) {
         e = launch_lora_dropout(X, n, dtype == NF4_DTYPE_BF16, drop, out, sms, st);
     } else if (X != out) {
-        const size_t bytes = static_cast<size_t>(n) * (dtype == NF4_DTYPE_BF16 ? 2 : 4);
         e = cudaMemcpyAsync(out, X, bytes, cudaMemcpyDeviceToDevice, st);
     }
     if (e != cudaSuccess) return fail(NF4_ERR_CUDA, "lora_dropout launch: %s", cudaGetErrorString(e));
