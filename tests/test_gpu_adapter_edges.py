@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from adapter_ref import check, reference
+from group_cases import CASES
 from test_gpu_dropout import rng_tensor
 from test_gpu_grouped import make, offsets_of
 
@@ -18,7 +19,8 @@ def nf():
 
 def compare(nf, E, N, K, r, counts, p, dq=True, first=0, behind=0, s=0.5, state=(3, 9)):
     """Forward and backward against the 64-bit results; rows outside the groups
-    hold NaN and keep what the outputs had."""
+    hold NaN and keep what the outputs had.  E None: the dense layer."""
+    dense, E = E is None, E or 1
     off, offsets = offsets_of(counts, first)
     M = off[-1] + behind
     w, W, d = make(nf, E, N, K, r, M, dq)
@@ -27,8 +29,14 @@ def compare(nf, E, N, K, r, counts, p, dq=True, first=0, behind=0, s=0.5, state=
     X, dY = torch.full_like(d["X"], float("nan")), torch.full_like(d["dY"], float("nan"))
     X[inside], dY[inside] = d["X"][inside], d["dY"][inside]
     Y, T, dX = torch.full_like(dY, 3.0), torch.full((M, r), 3.0, device="cuda"), torch.full_like(X, 3.0)
-    nf.qlora_grouped_fwd(w, d["A"], d["B"], s, X, offsets, p, rng, Y=Y, T=T)
-    _, dA, dB = nf.qlora_grouped_bwd(w, d["A"], d["B"], s, X, T, dY, offsets, p, rng, dX=dX)
+    if dense:
+        a, b = d["A"][0], d["B"][0]
+        nf.qlora_linear_dropout_fwd(w, a, b, s, X, p, rng, Y=Y, T=T)
+        _, dA, dB = nf.qlora_linear_dropout_bwd(w, a, b, s, X, T, dY, p, rng, dX=dX)
+        dA, dB = dA[None], dB[None]
+    else:
+        nf.qlora_grouped_fwd(w, d["A"], d["B"], s, X, offsets, p, rng, Y=Y, T=T)
+        _, dA, dB = nf.qlora_grouped_bwd(w, d["A"], d["B"], s, X, T, dY, offsets, p, rng, dX=dX)
     torch.cuda.synchronize()
     nf.device_status()
     ref = reference(W, d["A"], d["B"], d["X"], d["dY"], off, s, p, state)
@@ -37,6 +45,13 @@ def compare(nf, E, N, K, r, counts, p, dq=True, first=0, behind=0, s=0.5, state=
         assert (got[:off[0]] == 3.0).all() and (got[off[-1]:] == 3.0).all(), name
     check(dA, ref, "dA")
     check(dB, ref, "dB")
+
+
+@pytest.mark.parametrize("p,dq", [(0.0, False), (0.2, True)])
+@pytest.mark.parametrize("name", CASES)
+def test_pairs_that_walk_several_tiles_and_split_contractions(nf, name, p, dq):
+    E, N, K, r, rows = CASES[name][:5]
+    compare(nf, E, N, K, r, rows, p, dq)
 
 
 @pytest.mark.parametrize("p", [0.0, 0.25])
