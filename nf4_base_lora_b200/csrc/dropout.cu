@@ -56,7 +56,9 @@ __global__ void __launch_bounds__(kThreads) k_lora_dropout(const void* in, int64
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int64_t g = g0 + u * stride;
-            if (g < groups) {
+            if (g < groups && NF4_CHECK(in_span(src + g * kVec, 16 * kVec, in, n * (BF16 ? 2 : 4), 16) &&
+                                            in_span(dst + g * kVec, 16 * kVec, out, n * (BF16 ? 2 : 4), 16),
+                                        40)) {
                 uint32_t f[4];
                 gen.flags(static_cast<uint64_t>(g), f);
                 if constexpr (BF16) {

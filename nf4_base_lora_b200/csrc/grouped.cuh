@@ -558,6 +558,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             for (int e0 = 0; e0 < args.E; e0 += 32)
                 e += __popc(__ballot_sync(0xFFFFFFFFu, e0 + lane < args.E && s_first[min(e0 + lane, kGroups)] <= rt));
             if (rt >= s_first[args.E]) return false;
+            if (!NF4_CHECK(e >= 0 && e < args.E, 32)) return false;
             const int begin = min(max(s_off[e], 0), args.M);
             t.g.e = e;
             t.g.row0 = begin + (rt - s_first[e]) * s_size[e];
@@ -641,7 +642,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
     // goes with its tokens, completes the slot's phase without any.  The whole warp
     // calls it.
     auto load_codes = [&](const Tile& t, int it, int cs) {
-        if (elect_one()) {
+        if (elect_one() && NF4_CHECK(cs < LC && in_smem(codes_buf(cs), C::kCBytes, base, C::kSmem - 1024, 1024), 30)) {
             uint64_t* bar = &bar_codes[cs];
             if (is_main(t, it)) {
                 mbar_arrive_expect_tx(bar, C::kCBytes);
@@ -719,7 +720,10 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                     since = 0;
                 }
                 if (C::kWT) since = min(since + 1, DS);
-                if (elect_one()) {
+                if (elect_one() &&
+                    NF4_CHECK(ds < DS && in_smem(t_buf(ds), C::kTokBytes, base, C::kSmem - 1024, 1024) &&
+                                  in_smem(w_buf(C::kWT ? 0 : ds), C::kWBytes, base, C::kSmem - 1024, 1024),
+                              31)) {
                     if (rank == 0)
                         mbar_arrive_expect_tx(&bar_ready[ds], 2 * (bytes + (main_step ? 0 : C::kWBytes)));
                     const uint32_t bar = lead(&bar_ready[ds]);
@@ -961,9 +965,13 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             n_local = 8 * (qw >> 1) + i;
             cblk = ((i >> 1) + qw) & 1;
         }
-        const int dst_off = half * C::kW + (DX ? cblk * 8192 + n_local * 128 + ((n_local & 7) << 4)
+        int dst_off = half * C::kW + (DX ? cblk * 8192 + n_local * 128 + ((n_local & 7) << 4)
                                                : dt * 128 + ((dt & 7) << 4));
-        const int code_off = half * C::kCodes + (DX ? n_local * kCB + cblk : dt) * 32;
+        int code_off = half * C::kCodes + (DX ? n_local * kCB + cblk : dt) * 32;
+        if (!NF4_CHECK(code_off + (C::kUnits - 1) * C::kCodes + 32 <= C::kCBytes &&
+                           (C::kWT || (dst_off | 0x70) + 16 + (C::kUnits - 1) * C::kW <= C::kWBytes),
+                       38))
+            code_off = dst_off = 0;
         // The units' block scales are fetched one own step (several steps of the
         // pair) ahead: an 8-bit code and the second-level scale, or the fp32 scale.
         // With few tokens and an even number of blocks per row a step's two scales
@@ -993,6 +1001,10 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             for (int h = 0; h < C::kUnits; ++h)
                 k_end[h] = inside ? min(t.n_main, (kbs - half - h + C::kKS - 1) / C::kKS - t.kb0) : 0;
         };
+        // the encoded weight has this block's scales
+        auto have_block = [&](uint32_t b) {
+            return NF4_CHECK(b < static_cast<uint64_t>(args.E) * args.w_rows * args.w_blocks_per_row, 33);
+        };
         auto fetch = [&](int k) {
             Scale s;
             s.ok = 0;
@@ -1000,7 +1012,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             if (kPairs && pairs) {
                 s.q[0] = 0;
                 s.a2[0] = 0.0f;
-                if (k < k_end[0]) {
+                if (k < k_end[0] && have_block(b0) && have_block(b0 + 1)) {
                     s.ok = 1;
                     if (fp32_scales) {
                         const float2 two = __ldg(reinterpret_cast<const float2*>(args.absmax + b0));
@@ -1018,7 +1030,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                 s.q[h] = 0;
                 s.a2[h] = 0.0f;
                 const uint32_t b = b0 + (DX ? h * 64 * static_cast<uint32_t>(args.w_blocks_per_row) : h);
-                if ((!DROP || k >= 0) && k < k_end[h]) {
+                if ((!DROP || k >= 0) && k < k_end[h] && have_block(b)) {
                     s.ok |= 1u << h;
                     if (fp32_scales) {
                         s.a2[h] = __ldg(args.absmax + b);
@@ -1053,7 +1065,10 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             if (T <= 64 && j % 8 == 0 && j >= left) break;
-                            if (j < left && col < args.cols)
+                            if (j < left && col < args.cols &&
+                                NF4_CHECK(in_span(dst + static_cast<int64_t>(j) * args.cols, 4, args.part,
+                                                  static_cast<int64_t>(args.splits) * args.M * args.cols * 4, 4),
+                                          34))
                                 dst[static_cast<int64_t>(j) * args.cols] = __uint_as_float(v[j]);
                         }
                     } else {
@@ -1065,7 +1080,10 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
                             if (T <= 64 && j % 8 == 0 && j >= left) break;
                             const uint32_t own = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
                             const uint32_t two = __byte_perm(own, __shfl_xor_sync(0xFFFFFFFFu, own, 1), sel);
-                            if (j < rows) *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(j) * args.cols) = two;
+                            if (j < rows && NF4_CHECK(in_span(dst + static_cast<int64_t>(j) * args.cols, 4, args.out,
+                                                              static_cast<int64_t>(args.M) * args.cols * 2, 4),
+                                                      35))
+                                *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(j) * args.cols) = two;
                         }
                     }
                 }
@@ -1154,6 +1172,7 @@ __global__ void __launch_bounds__(GroupGemmConfig<DX, T>::kThreads, GroupGemmCon
             if (__any_sync(0xFFFFFFFFu, !ok)) break;  // the warp stays together
             it += C::kTeams;
             ahead = fetch(it - main0(t));
+            if (!NF4_CHECK(cs < LC && ds < DS, 36)) break;  // of the whole warp
             // a unit outside the weight has a zero scale and decodes to zeros
             if (C::kWT && main_step) {
                 tc_fence_after();
@@ -1217,6 +1236,10 @@ __global__ void k_group_sum(const int32_t* offsets, int E, int M, int cols, int 
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
         const float4* p = reinterpret_cast<const float4*>(part) + static_cast<int64_t>(lo) * quads + i;
+        if (!NF4_CHECK(in_span(p + (splits - 1) * slice, 16, part, splits * slice * 16, 16) &&
+                           in_span(out + 4 * (static_cast<int64_t>(lo) * quads + i), 8, out, slice * 8, 8),
+                       37))
+            continue;
         float4 v = __ldcg(p);
         for (int z = 1; z < splits; ++z) {
             const float4 x = __ldcg(p + z * slice);

@@ -79,18 +79,21 @@ struct RankArgs {
 };
 
 // v[0 .. 7] = columns j .. j + 7 of a row of T or V: the 16-bit pair, zero beyond
-// r, and the fp32 value.
-__device__ __forceinline__ void store_pair(float (&v)[8], int64_t row, int j, int r, int r64, uint16_t* pair,
-                                           float* out32) {
+// r, and the fp32 value; the arrays have M rows.
+__device__ __forceinline__ void store_pair(float (&v)[8], int64_t row, int j, int64_t M, int r, int r64,
+                                           uint16_t* pair, float* out32) {
     float hi[8], lo[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
         if (j + u >= r) v[u] = 0.0f;
         hi[u] = bf16_high_part(v[u]);
         lo[u] = v[u] - hi[u];
-        if (out32 != nullptr && j + u < r) out32[row * r + j + u] = v[u];
+        if (out32 != nullptr && j + u < r && NF4_CHECK(in_span(out32 + row * r + j + u, 4, out32, M * r * 4, 4), 20))
+            out32[row * r + j + u] = v[u];
     }
     uint16_t* dst = pair + row * 2 * r64 + j;
+    if (!NF4_CHECK(in_span(dst, 16, pair, M * 4 * r64, 16) && in_span(dst + r64, 16, pair, M * 4 * r64, 16), 21))
+        return;
     *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3]),
                                                 pack_bf16x2(hi[4], hi[5]), pack_bf16x2(hi[6], hi[7]));
     *reinterpret_cast<uint4*>(dst + r64) = make_uint4(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]),
@@ -279,7 +282,11 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
                 uint8_t* b_buf = a_buf + args.a_bytes;
                 const int k = 64 * (step0 + it);
                 mbar_arrive_expect_tx(bar, slot_bytes);
-                if constexpr (!TOK) {
+                if (!NF4_CHECK(in_smem(a_buf, slot_bytes, base, static_cast<int64_t>(LS) * slot_bytes, 1024) &&
+                                   args.a_bytes % 1024 == 0 && (args.r64 & 7) == 0,
+                               22)) {
+                    // nothing is copied, and the wait for it runs out
+                } else if constexpr (!TOK) {
                     tma_load_2d(a_buf, &map_a, bar, k, g.row0);
                     if constexpr (MODE == RANK_T) {
                         tma_load_3d(b_buf, &map_b, bar, k, 0, g.e);
@@ -407,6 +414,7 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
                             inside = rr < rows_kept;
                         }
                         uint4* at = reinterpret_cast<uint4*>(a + off);
+                        if (!NF4_CHECK(in_smem(at, 16, a, args.a_bytes, 16), 23)) continue;
                         uint4 v = *at;
                         uint32_t m[4];
                         gen.masks(gi, m);
@@ -429,7 +437,9 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
                         const int chunk = kFirst + p / per, rem = p % per;
                         uint8_t* src =
                             chunk < kOutRows / 64 ? a + chunk * 8192 : b_buf + (chunk - kOutRows / 64) * 8192;
-                        *reinterpret_cast<uint4*>(src + tail_rows * 128 + rem * 16) = make_uint4(0, 0, 0, 0);
+                        src += tail_rows * 128 + rem * 16;
+                        if (NF4_CHECK(in_smem(src, 16, a, slot_bytes, 16), 23))
+                            *reinterpret_cast<uint4*>(src) = make_uint4(0, 0, 0, 0);
                     }
                 }
                 fence_proxy_async_smem();
@@ -487,19 +497,27 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
                     float x[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(v[j]) * args.alpha;
-                    store_pair(x, row, cc, args.r, args.r64, args.pair, args.out32);
+                    store_pair(x, row, cc, args.M, args.r, args.r64, args.pair, args.out32);
                 } else if constexpr (!TOK) {
                     float* dst = args.part + blockIdx.z * args.part_slice + static_cast<int64_t>(row) * args.rn + cc;
+                    if (!NF4_CHECK(in_span(dst, 32, args.part, gridDim.z * args.part_slice * 4, 16), 24)) continue;
                     *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
                     *reinterpret_cast<uint4*>(dst + 4) = make_uint4(v[4], v[5], v[6], v[7]);
                 } else if constexpr (MODE == RANK_DB) {
                     if (!direct) {
                         float* dst = args.part + static_cast<int64_t>(part.slot + part.part) * args.part_slice +
                                      static_cast<int64_t>(row) * args.rn + cc;
+                        if (!NF4_CHECK(in_span(dst, 32, args.part, args.slots * args.part_slice * 4, 16), 24)) continue;
                         *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
                         *reinterpret_cast<uint4*>(dst + 4) = make_uint4(v[4], v[5], v[6], v[7]);
                     } else {
                         uint16_t* dst = args.out + (static_cast<int64_t>(g.e) * args.rows + row) * args.r + cc;
+                        if (cc >= args.r) continue;
+                        if (!NF4_CHECK(in_span(dst, 2 * min(8, args.r - cc), args.out,
+                                               static_cast<int64_t>(args.E) * args.rows * args.r * 2,
+                                               args.r % 8 == 0 ? 16 : 2),
+                                       25))
+                            continue;
                         uint16_t o[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
@@ -520,13 +538,21 @@ __global__ void __launch_bounds__(RankConfig<MODE, DROP>::kThreads, 2)
                         float* dst = args.part + static_cast<int64_t>(part.slot + part.part) * args.part_slice +
                                      static_cast<int64_t>(cc) * args.rows + row;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) dst[static_cast<int64_t>(j) * args.rows] = __uint_as_float(v[j]);
+                        for (int j = 0; j < 8; ++j)
+                            if (NF4_CHECK(in_span(dst + static_cast<int64_t>(j) * args.rows, 4, args.part,
+                                                  args.slots * args.part_slice * 4, 4),
+                                          24))
+                                dst[static_cast<int64_t>(j) * args.rows] = __uint_as_float(v[j]);
                     } else {
                         uint16_t* dst = args.out + (static_cast<int64_t>(g.e) * args.r + cc) * args.rows + row;
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             if (cc + j < args.r) {
                                 uint16_t* d = dst + static_cast<int64_t>(j) * args.rows;
+                                if (!NF4_CHECK(in_span(d, 2, args.out,
+                                                       static_cast<int64_t>(args.E) * args.rows * args.r * 2, 2),
+                                               25))
+                                    continue;
                                 float x = __uint_as_float(v[j]) * args.alpha;
                                 if (args.accumulate) x += bf16_bits_to_float(*d);
                                 *d = bf16_bits(x);
@@ -581,6 +607,7 @@ __global__ void k_rank_rows_sum(const RankRowsSumArgs a) {
         if (j < a.rn) {
             const float* p = a.part + row * a.rn + j;
             for (int z = 0; z < a.splits; ++z, p += a.slice) {
+                if (!NF4_CHECK(in_span(p, 32, a.part, a.splits * a.slice * 4, 16), 26)) break;
                 const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
                 const float4 y = __ldcg(reinterpret_cast<const float4*>(p) + 1);
                 v[0] += x.x;
@@ -595,7 +622,7 @@ __global__ void k_rank_rows_sum(const RankRowsSumArgs a) {
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) v[u] *= a.alpha;
-        store_pair(v, row, j, a.r, a.r64, a.pair, a.out32);
+        store_pair(v, row, j, a.M, a.r, a.r64, a.pair, a.out32);
     }
 }
 
@@ -612,7 +639,7 @@ __global__ void k_rank_pair(const float* __restrict__ src, int64_t M, int r, int
         float v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) v[u] = j + u < r ? __ldcg(src + row * r + j + u) : 0.0f;
-        store_pair(v, row, j, r, r64, pair, nullptr);
+        store_pair(v, row, j, M, r, r64, pair, nullptr);
     }
 }
 
@@ -692,6 +719,11 @@ __global__ void __launch_bounds__(256)
         uint16_t* dst = out + static_cast<int64_t>(s_e[k]) * rows * r;
         const int64_t outer = total < (int64_t(1) << 31) ? static_cast<int>(i) / inner : i / inner;
         const float* at = part + s_slot[k] * slice + outer * ld + (i - outer * inner) * VEC;
+        if (!NF4_CHECK(in_span(at, 4 * VEC, part, slots * slice * 4, 4 * VEC) &&
+                           in_span(at + (parts - 1) * slice, 4 * VEC, part, slots * slice * 4, 4 * VEC) &&
+                           in_span(dst + i * VEC, 2 * VEC, out, static_cast<int64_t>(E) * rows * r * 2, 2 * VEC),
+                       27))
+            continue;
         float v[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) v[j] = 0.0f;
