@@ -337,6 +337,13 @@ int qlora_linear_dropout_bwd(const nf4_tensor* w, const uint16_t* A, const uint1
  * n_experts * d_out * d_in / 64 < 2^32; no output overlaps an input or another
  * output; else as for
  * qlora_linear_fwd / _bwd, ws >= the sizes below (d_out of one expert).
+ * The other calls take one adapter per weight, so an expert goes to them (to
+ * nf4_merge_lora, say) as an nf4_tensor {d_out, d_in} of its own whose pointers
+ * are the stacked ones moved by what n = e * d_out * d_in weights take: codes by
+ * n / 2, absmax by n / 64, or qscale by n / 64 and scale2 by n / 16384, with the
+ * same scale_mean.  With double quantisation d_out * d_in has to be a multiple of
+ * 65536 for that: groups of 256 scales are not shared then, and scale2 stays
+ * aligned.  lora_adamw_step takes the stacked adapters as they are.
  */
 size_t qlora_grouped_fwd_workspace_bytes(int64_t M, int n_experts, int64_t d_out, int64_t d_in, int r);
 size_t qlora_grouped_bwd_workspace_bytes(int64_t M, int n_experts, int64_t d_out, int64_t d_in, int r);

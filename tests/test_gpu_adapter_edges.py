@@ -1,5 +1,7 @@
 """Edges of the dropout and grouped layers that their kernels treat apart, on the
 GPU against 64-bit results."""
+import ctypes
+
 import pytest
 import torch
 
@@ -240,3 +242,26 @@ def test_gradients_over_many_rows_keep_their_precision(nf, which):
     got = grad.double() - before
     mean = (((got.t() if which == "dB" else got) - ref) / ref).mean()
     assert abs(float(mean)) <= 1024 * 2.0 ** -25 + 2.0 ** -16, float(mean)
+
+
+@pytest.mark.parametrize("dq,N,K", [(True, 256, 256), (True, 64, 2048), (False, 24, 192)])
+def test_an_expert_as_a_tensor_of_its_own(nf, dq, N, K):
+    """The pointers that the header gives for one expert of a stack: merged with its
+    adapter it is its weight plus s B A, rounded once to fp32 (64-bit sums)."""
+    E, r, s = 3, 5, 0.75
+    w, W, d = make(nf, E, N, K, r, 1, dq)
+    full = w.struct
+    for e in range(E):
+        n = e * N * K
+        one = nf.Nf4TensorStruct(N, K, full.codes + n // 2)
+        if dq:
+            one.qscale, one.scale2 = full.qscale + n // 64, full.scale2 + 4 * (n // 16384)
+            one.scale_mean = full.scale_mean
+        else:
+            one.absmax = full.absmax + 4 * (n // 64)
+        out = torch.empty((N, K), device="cuda")
+        A, B = d["A"][e], d["B"][e]
+        assert nf.lib.nf4_merge_lora(ctypes.byref(one), A.data_ptr(), B.data_ptr(), r, s, out.data_ptr(),
+                                     torch.cuda.current_stream().cuda_stream) == 0
+        ref = W[e].double() + s * (B.double() @ A.double())
+        assert ((out.double() - ref).abs() <= 2.0 ** -24 * ref.abs() * 1.001 + 1e-15).all()
