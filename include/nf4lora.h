@@ -334,9 +334,10 @@ int qlora_linear_dropout_bwd(const nf4_tensor* w, const uint16_t* A, const uint1
  * (a call that has nothing to compute -- M = 0, or no output asked for -- does
  * not read them).
  * Requirements: 1 <= n_experts <= NF4_MAX_EXPERTS, d_out % 8 == 0,
- * n_experts * d_out * d_in / 64 < 2^32; no output overlaps an input or another
- * output; else as for
- * qlora_linear_fwd / _bwd, ws >= the sizes below (d_out of one expert).
+ * n_experts * d_out * d_in / 64 < 2^32, n_experts * d_out <= 2^31 - 64 (both
+ * for the dropout layer too, as one expert); no output overlaps an input or
+ * another output; else as for qlora_linear_fwd / _bwd, ws >= the sizes below
+ * (d_out of one expert).
  * The other calls take one adapter per weight, so an expert goes to them (to
  * nf4_merge_lora, say) as an nf4_tensor {d_out, d_in} of its own whose pointers
  * are the stacked ones moved by what n = e * d_out * d_in weights take: codes by

@@ -337,13 +337,15 @@ int lora_dropout(const void* X, int64_t n, int dtype, const lora_dropout_params*
     return ok();
 }
 
-// The kernels of these layers number a weight's 64-element blocks in 32 bits.
-static bool blocks_fit(int64_t rows, int64_t d_in) { return rows * (d_in / 64) < (int64_t(1) << 32); }
+// The kernels of these layers number a weight's 64-element blocks in 32 bits, and
+// count its rows in whole steps of 64 in 31.
+static bool blocks_fit(int64_t rows, int64_t d_in) {
+    return rows <= (int64_t(1) << 31) - 64 && rows * (d_in / 64) < (int64_t(1) << 32);
+}
 
 static bool valid_group_shape(int64_t M, int n_experts, int64_t d_out, int64_t d_in, int r) {
     return valid_weight_shape(d_out, d_in) && M >= 1 && M < (int64_t(1) << 31) && r >= 1 && r <= 256 &&
-           n_experts >= 1 && n_experts <= NF4_MAX_EXPERTS && d_out * n_experts < (int64_t(1) << 31) &&
-           blocks_fit(d_out * n_experts, d_in);
+           n_experts >= 1 && n_experts <= NF4_MAX_EXPERTS && blocks_fit(d_out * n_experts, d_in);
 }
 
 size_t qlora_linear_dropout_fwd_workspace_bytes(int64_t M, int64_t d_out, int64_t d_in, int r) {
@@ -380,8 +382,8 @@ static int check_group(const nf4_tensor* w, int n_experts, bool grouped, const i
         return fail(NF4_ERR_UNSUPPORTED_SHAPE, "d_out = %lld must be a multiple of 8",
                     (long long)(w->d_out / n_experts));
     if (!blocks_fit(w->d_out, w->d_in))
-        return fail(NF4_ERR_UNSUPPORTED_SHAPE, "%lld x %lld: 2^32 blocks or more", (long long)w->d_out,
-                    (long long)w->d_in);
+        return fail(NF4_ERR_UNSUPPORTED_SHAPE, "%lld x %lld: 2^32 blocks or more, or more than 2^31 - 64 rows",
+                    (long long)w->d_out, (long long)w->d_in);
     rc = check_layer_common(w, A, B, r, scaling, M);
     if (rc) return rc;
     DropArgs drop;

@@ -29,7 +29,7 @@ def golden_table(name):
 
 # These modules pass made-up addresses to entry points and expect the call to end at
 # the check for a device.  Where there is one, the kernels would run on them.
-MADE_UP_ADDRESSES = ("test_abi", "test_adapter_host", "test_adapter_overlap")
+MADE_UP_ADDRESSES = ("test_abi", "test_adapter_host", "test_adapter_limits", "test_adapter_overlap")
 
 
 def skip_made_up_addresses(items, have_device):
