@@ -326,7 +326,7 @@ def qlora_linear_bwd(w: NF4Tensor, A: torch.Tensor, B: torch.Tensor, scaling: fl
 # the host is kept to a few microseconds: the stream as the raw handle (the
 # public accessor builds a stream object), a device switch only where it is
 # needed, messages only where a check fails.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # not there in a torch without CUDA
 _BF16, _F32 = torch.bfloat16, torch.float32
 
 
