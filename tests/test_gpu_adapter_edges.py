@@ -1,6 +1,10 @@
 """Edges of the dropout and grouped layers that their kernels treat apart, on the
 GPU against 64-bit results."""
 import ctypes
+import os
+import subprocess
+import sys
+import threading
 
 import pytest
 import torch
@@ -265,3 +269,130 @@ def test_an_expert_as_a_tensor_of_its_own(nf, dq, N, K):
                                      torch.cuda.current_stream().cuda_stream) == 0
         ref = W[e].double() + s * (B.double() @ A.double())
         assert ((out.double() - ref).abs() <= 2.0 ** -24 * ref.abs() * 1.001 + 1e-15).all()
+
+
+@pytest.mark.parametrize("M", [5, 90, 700])
+def test_layers_of_every_kind_in_one_chain(nf, M):
+    """The kernels of all layers are programmatic dependents of one another.  Plain,
+    dropout and grouped layers in turn, forward and backward in one workspace, each
+    on what the one before wrote: synchronised after every call, back to back and
+    replayed from a graph, the same bits."""
+    D, r, E, p, s = 512, 16, 4, 0.1, 0.5
+    w, W, d = make(nf, 1, D, D, r, M)
+    we, _, de = make(nf, E, D, D, r, M, seed=1)
+    A, B = d["A"][0], d["B"][0]
+    rng = rng_tensor((4, 4))
+    _, offsets = offsets_of([M // 3, 0, M - M // 3, 0])
+    need = max(nf.qlora_fwd_workspace_bytes(M, D, D, r), nf.qlora_bwd_workspace_bytes(M, D, D, r),
+               nf.qlora_grouped_fwd_workspace_bytes(M, E, D, D, r), nf.qlora_grouped_bwd_workspace_bytes(M, E, D, D, r),
+               nf.qlora_linear_dropout_fwd_workspace_bytes(M, D, D, r),
+               nf.qlora_linear_dropout_bwd_workspace_bytes(M, D, D, r))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    new = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    h = [d["X"]] + [new(M, D) for _ in range(6)]
+    g = [d["dY"]] + [new(M, D) for _ in range(6)]
+    t = [torch.empty((M, r), device="cuda") for _ in range(6)]
+    dA = [new(E, r, D) if i % 3 == 2 else new(r, D) for i in range(6)]
+    dB = [new(E, D, r) if i % 3 == 2 else new(D, r) for i in range(6)]
+
+    def chain(after):
+        for i in range(6):
+            if i % 3 == 0:
+                nf.qlora_linear_fwd(w, A, B, s, h[i], Y=h[i + 1], T=t[i], workspace=ws)
+            elif i % 3 == 1:
+                nf.qlora_linear_dropout_fwd(w, A, B, s, h[i], p, rng, Y=h[i + 1], T=t[i], workspace=ws)
+            else:
+                nf.qlora_grouped_fwd(we, de["A"], de["B"], s, h[i], offsets, p, rng, Y=h[i + 1], T=t[i], workspace=ws)
+            after()
+        for k, i in enumerate(reversed(range(6))):
+            out = dict(dX=g[k + 1], dA=dA[i], dB=dB[i], workspace=ws)
+            if i % 3 == 0:
+                nf.qlora_linear_bwd(w, A, B, s, h[i], t[i], g[k], **out)
+            elif i % 3 == 1:
+                nf.qlora_linear_dropout_bwd(w, A, B, s, h[i], t[i], g[k], p, rng, **out)
+            else:
+                nf.qlora_grouped_bwd(we, de["A"], de["B"], s, h[i], t[i], g[k], offsets, p, rng, **out)
+            after()
+    everything = [*h[1:], *g[1:], *t, *dA, *dB]
+    chain(torch.cuda.synchronize)
+    first = [v.clone() for v in everything]
+    assert all(torch.isfinite(v).all() for v in first)
+
+    def same():
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(everything, first))
+        for v in everything:
+            v.fill_(7.0)
+    same()
+    for _ in range(5):
+        chain(lambda: None)
+        same()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(lambda: None)
+        chain(lambda: None)
+    for _ in range(5):
+        graph.replay()
+        same()
+    nf.device_status()
+
+
+FIRST_CALL = """
+import torch, sys
+sys.path[:0] = ["tests"]
+import nf4_base_lora_b200 as nf
+from test_gpu_grouped import make, offsets_of
+w, W, d = make(nf, 2, 256, 192, 12, 40)
+off, offsets = offsets_of([30, 10])
+rng = torch.tensor([1, 2], device="cuda")
+def step():
+    x = nf.lora_dropout(d["X"], 0.2, rng)
+    y, t = nf.qlora_grouped_fwd(w, d["A"], d["B"], 1.0, x, offsets, 0.2, rng)
+    return y, t, *nf.qlora_grouped_bwd(w, d["A"], d["B"], 1.0, x, t, d["dY"], offsets, 0.2, rng)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = step()
+graph.replay()
+eager = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, eager))
+nf.device_status()
+print("same")
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and "same" in out.stdout, out.stderr[-3000:]
+
+
+def test_two_host_threads_at_once(nf):
+    """Each thread its own stream, data and workspaces; the same bits as alone."""
+    sets = [make(nf, 3, 256, 320, 16, 150, seed=i) for i in range(2)]
+    _, offsets = offsets_of([70, 0, 80])
+    rng = rng_tensor((5, 5))
+
+    def step(w, d):
+        y, t = nf.qlora_grouped_fwd(w, d["A"], d["B"], 1.0, d["X"], offsets, 0.1, rng)
+        return (nf.lora_dropout(d["X"], 0.1, rng), y, t,
+                *nf.qlora_grouped_bwd(w, d["A"], d["B"], 1.0, d["X"], t, d["dY"], offsets, 0.1, rng))
+    alone = [step(w, d) for w, _, d in sets]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got = step(sets[i][0], sets[i][2])
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, alone[i])):
+                    wrong.append(i)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong
+    nf.device_status()
